@@ -14,6 +14,8 @@ Entry points (same names as the C ABI, without the ``qlora_`` prefix):
   linear_fwd(x, w, A, B, alpha)   -> (h, us)
   linear_bwd(dh, x, us, w, A, B, alpha) -> (dx, dA, dB)
   linear_fwd_group(problems), linear_bwd_group(problems)   (n projections issued together)
+  token_slots(lengths, slots, n_tokens)           -> ids (the adapter slot of every token)
+  linear_fwd_slots(x, w, A, B, scale, ids)        -> h   (one adapter per request over a shared base)
   workspace_size(op, M, in_features, out_features, r)
   last_device_status(), set_wait_timeout_ns(ns), selftest_wait_timeout()
 """
@@ -35,6 +37,7 @@ __all__ = [
     "timing_enable", "timing_reset", "timing_collect", "KERNEL_NAMES", "merge_adapter",
     "quantize_codebook", "dequantize_codebook", "CODEBOOK_NF4", "CODEBOOK_INT4",
     "linear_fwd_dropout", "linear_bwd_dropout", "pack_keep_mask", "OP_LINEAR_FWD_DROPOUT", "OP_LINEAR_BWD_DROPOUT",
+    "token_slots", "linear_fwd_slots", "OP_LINEAR_FWD_SLOTS",
     "OP_QUANTIZE", "OP_DEQUANTIZE", "OP_LINEAR_FWD", "OP_LINEAR_BWD",
     "quantize_shard_plan", "quantize_shard_workspace_size", "quantize_nf4_shard_local", "quantize_nf4_shard_finish",
 ]
@@ -105,6 +108,8 @@ def load():
         "qlora_dequantize_codebook": (I, [I, W, P, P]),
         "qlora_linear_fwd_dropout": (I, [P, I64, W, P, P, I, F, P, F, P, P, P, SZ, P]),
         "qlora_linear_bwd_dropout": (I, [P, P, P, I64, W, P, P, I, F, P, F, P, P, P, P, SZ, P]),
+        "qlora_token_slots": (I, [P, P, I64, I64, P, P]),
+        "qlora_linear_fwd_slots": (I, [P, I64, W, P, P, I64, I, P, P, P, P, SZ, P]),
         "qlora_quantize_shard_plan": (I, [I64, I, I, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64),
                                           ctypes.POINTER(ctypes.c_int64)]),
         "qlora_quantize_shard_workspace_size": (SZ, [I64, I64]),
@@ -148,6 +153,14 @@ def _need(t, dtype, name, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _one_device(*tensors):
+    """All tensors live on the current device, whose stream the call uses."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
 
 
 @dataclass
@@ -516,6 +529,48 @@ def linear_bwd_dropout(dh, x, us, w: NF4Weight, A, B, alpha: float, keep_bits, p
     return dx, dA, dB
 
 
+OP_LINEAR_FWD_SLOTS = 6
+
+
+def token_slots(lengths, slots, n_tokens: int, out=None) -> torch.Tensor:
+    """int32 [n_tokens]: the adapter slot of every token of requests that lie
+    one after another (lengths and slots int32 [n_requests]); -1 for the
+    tokens behind the last request."""
+    _need(lengths, torch.int32, "lengths")
+    _need(slots, torch.int32, "slots", lengths.shape)
+    if lengths.dim() != 1:
+        raise ValueError("lengths must have one dimension")
+    ids = out if out is not None else torch.empty(n_tokens, dtype=torch.int32, device=lengths.device)
+    _need(ids, torch.int32, "out", (n_tokens,))
+    _one_device(lengths, slots, ids)
+    _check(load().qlora_token_slots(_ptr(lengths), _ptr(slots), lengths.shape[0], int(n_tokens), _ptr(ids),
+                                    _stream()), "qlora_token_slots")
+    return ids
+
+
+def linear_fwd_slots(x, w: NF4Weight, A, B, scale, ids, h=None, workspace=None):
+    """The layer with one adapter per token: h[m] = W0 x[m] + scale[a] B[a] A[a] x[m],
+    a = ids[m] (see :func:`token_slots`); a token with a slot outside [0, n)
+    gets the base product alone.  A bf16 [n, r, in], B bf16 [n, out, r],
+    scale fp32 [n], ids int32 [M]; returns h bf16 [M, out]."""
+    M = x.shape[0]
+    n, r = A.shape[0], A.shape[1]
+    _need(x, torch.bfloat16, "x", (M, w.cols))
+    _need(A, torch.bfloat16, "A", (n, r, w.cols))
+    _need(B, torch.bfloat16, "B", (n, w.rows, r))
+    _need(scale, torch.float32, "scale", (n,))
+    _need(ids, torch.int32, "ids", (M,))
+    h = h if h is not None else torch.empty((M, w.rows), dtype=torch.bfloat16, device=x.device)
+    _need(h, torch.bfloat16, "h", (M, w.rows))
+    _one_device(x, w.codes, A, B, scale, ids, h)
+    ws = _workspace(workspace_size(OP_LINEAR_FWD_SLOTS, M, w.cols, w.rows, r), x.device, workspace)
+    cw = w._c()
+    _check(load().qlora_linear_fwd_slots(_ptr(x), M, ctypes.byref(cw), _ptr(A), _ptr(B), n, r, _ptr(scale), _ptr(ids),
+                                         _ptr(h), _ptr(ws), ws.numel() if ws is not None else 0, _stream()),
+           "qlora_linear_fwd_slots")
+    return h
+
+
 def last_device_status() -> int:
     """Synchronize the current stream, read and clear the device error flag."""
     return int(load().qlora_last_device_status(_stream()))
@@ -531,7 +586,7 @@ def selftest_wait_timeout() -> int:
 
 KERNEL_NAMES = ("quantize_blocks", "scale_mean_tree", "dq_scales", "dequantize", "gemm_fwd", "gemm_dx",
                 "gemv", "gemv_finalize", "lora_rowwise", "lora_rowwise_du", "lora_colwise",
-                "merge_adapter", "dropout_dx", "lora_fewtok", "lora_pad")
+                "merge_adapter", "dropout_dx", "lora_fewtok", "lora_pad", "token_slots", "slots_us", "slots_gemm")
 
 
 def timing_enable(on: bool = True) -> bool:

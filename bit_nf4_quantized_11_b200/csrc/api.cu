@@ -25,6 +25,8 @@
 #include "lora_sm100.cuh"
 #include "pad.cuh"
 #include "fewtok.cuh"
+#include "slots.cuh"
+#include "gemm_slots_sm100.cuh"
 
 namespace qnf4_host {
 void build_codebook(float levels[16], float thresholds[15]);
@@ -175,13 +177,14 @@ bool make_tmap_bf16(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t c
 }
 
 // 2-D byte tensor [rows, cols] (packed NF4 codes, cols = in / 2), box
-// {128 bytes, 256 rows}, 128B swizzle, out-of-range bytes read as zero.
-bool make_tmap_codes(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols) {
+// {128 bytes, box_rows rows}, 128B swizzle, out-of-range bytes read as zero.
+bool make_tmap_codes(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols,
+                     uint32_t box_rows = qnf4::kGvRows) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(qnf4::kGvStageK / 2), static_cast<cuuint32_t>(qnf4::kGvRows)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(qnf4::kGvStageK / 2), box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -670,6 +673,8 @@ int launch_lora_grads(const uint16_t* dh, const uint16_t* us, const uint16_t* x,
 }
 
 // ------------------------------------------------------------------ validation
+constexpr int64_t kMaxTokens = (1ll << 31) - 1024;     // token and rank-row indices fit 32 bits
+
 bool weight_ok(const qlora_nf4_weight* w) {
   return w != nullptr && w->codes && w->q8 && w->step2 && w->mean && aligned(w->codes, 16) &&
          aligned(w->q8, 16) && aligned(w->step2, 16) && aligned(w->mean, 16);
@@ -679,7 +684,7 @@ int check_linear_shapes(int64_t M, const qlora_nf4_weight* w, int r) {
   if (M < 1 || w->rows < 64 || w->cols < 64) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (w->cols % 64 != 0 || w->rows % 64 != 0) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (r < 1 || r > 256) return QLORA_ERR_UNSUPPORTED_SHAPE;
-  if (M > (1ll << 31) - 1024 || w->rows > (1ll << 30) || w->cols > (1ll << 30))
+  if (M > kMaxTokens || w->rows > (1ll << 30) || w->cols > (1ll << 30))
     return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (w->rows * w->cols > (1ll << 40)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
@@ -907,6 +912,123 @@ int check_bwd_args(const uint16_t* dh, const uint16_t* x, const uint16_t* us, in
   return check_linear_shapes(M, w, r);
 }
 
+// ------------------------------------------------------------------ one adapter per request
+// Workspace of linear_fwd_slots: us [M, r8] bf16.
+size_t slots_ws(int64_t M, int r) { return round256(static_cast<size_t>(M) * padded_rank(r) * 2); }
+
+int launch_slots_us(const uint16_t* x, const uint16_t* A, const float* scale, const int32_t* ids, int64_t M,
+                    int64_t in, int64_t n_adapters, int r, uint16_t* us, cudaStream_t st) {
+  const int r8 = padded_rank(r);
+  {
+    LaunchTimer lt_("slots_us", st);
+    qnf4::slots_us_kernel<<<static_cast<unsigned>(cdiv(M * (r8 / 8), 8)), 256, 0, st>>>(x, A, scale, ids, M, in,
+                                                                                      n_adapters, r, r8, us);
+  }
+  QLORA_CUDA_TRY(cudaGetLastError());
+  return QLORA_OK;
+}
+
+// Clusters of ks CTAs of the kernel that the device holds at once, looked up
+// once per device (at the largest shared-memory size; one CTA per SM at any).
+int slots_gemm_clusters(int ks) {
+  static std::atomic<int> cache[kMaxDevices][9];
+  const int dev = current_device();
+  const int c = cache[dev][ks].load(std::memory_order_relaxed);
+  if (c > 0) return c;
+  const int smem = qnf4::sg_smem_bytes(qnf4::kSgMaxN);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1, static_cast<unsigned>(ks), 1);
+  cfg.blockDim = dim3(qnf4::kSgThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = static_cast<unsigned>(ks);
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (set_max_smem(reinterpret_cast<const void*>(qnf4::slots_gemm_kernel), smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, qnf4::slots_gemm_kernel, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    return std::max(1, device_sm_count() / ks);
+  }
+  cache[dev][ks].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Split of the K axis: the cluster size whose rounds of clusters, each of
+// (units per CTA + the fixed cost of a CTA in units), come out shortest.
+int slots_gemm_split(int64_t tiles, int n_units) {
+  constexpr int kFixed = 4;                    // prologue, epilogue and reduction, in 256-column units
+  int best = 1;
+  int64_t best_cost = 0;
+  for (int ks = 1; ks <= 8 && ks <= n_units; ++ks) {
+    const int64_t cost = cdiv(tiles, slots_gemm_clusters(ks)) * (cdiv(n_units, ks) + kFixed);
+    if (ks == 1 || cost < best_cost) {
+      best = ks;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, const uint16_t* A,
+                          const uint16_t* B, int64_t n_adapters, int r, const float* scale, const int32_t* ids,
+                          uint16_t* h, void* workspace, cudaStream_t st) {
+  const int64_t in = w->cols, out = w->rows;
+  uint16_t* us = static_cast<uint16_t*>(workspace);
+  const int rc = launch_slots_us(x, A, scale, ids, M, in, n_adapters, r, us, st);
+  if (rc != QLORA_OK) return rc;
+  // equal token tiles of at most 256, in whole UMMA steps of 16
+  const int64_t tok_tiles = cdiv(M, qnf4::kSgMaxN);
+  const int N = static_cast<int>(cdiv(cdiv(M, tok_tiles), 16) * 16);
+  const int64_t tiles = cdiv(out, qnf4::kSgRows) * tok_tiles;
+  if (tiles > kMaxTokens) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  qnf4::SlotsGemmArgs a{};
+  a.q8 = w->q8;
+  a.step2 = w->step2;
+  a.mean = w->mean;
+  a.us = us;
+  a.B = B;
+  a.ids = ids;
+  a.h = h;
+  a.n_adapters = n_adapters;
+  a.M = static_cast<int>(M);
+  a.out = static_cast<int>(out);
+  a.K = static_cast<int>(in);
+  a.r = r;
+  a.r8 = padded_rank(r);
+  a.N = N;
+  a.L = tables().L;
+  a.timeout_ns = g_timeout_ns.load();
+  CUtensorMap tm_codes, tm_x;
+  if (!make_tmap_codes(&tm_codes, w->codes, static_cast<uint64_t>(out), static_cast<uint64_t>(in / 2), qnf4::kSgRows) ||
+      !make_tmap_bf16(&tm_x, x, static_cast<uint64_t>(M), static_cast<uint64_t>(in), static_cast<uint32_t>(N)))
+    return QLORA_ERR_CUDA;
+  const int ks = slots_gemm_split(tiles, static_cast<int>(cdiv(in, 256)));
+  const int smem = qnf4::sg_smem_bytes(N);
+  QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(qnf4::slots_gemm_kernel), smem));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(ks), 1);
+  cfg.blockDim = dim3(qnf4::kSgThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = static_cast<unsigned>(ks);
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ks > 1 ? 1 : 0;
+  {
+    LaunchTimer lt_("slots_gemm", st);
+    QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, qnf4::slots_gemm_kernel, tm_codes, tm_x, a));
+  }
+  QLORA_CUDA_TRY(cudaGetLastError());
+  return QLORA_OK;
+}
+
 // The rank-r work of a projection moves to the low-priority stream only on
 // the path where it is separate from the GEMM (M > 16, r % 8 == 0).
 bool group_split(const qlora_linear_problem& p) { return p.M > 16 && p.r % 8 == 0; }
@@ -971,6 +1093,9 @@ size_t qlora_workspace_size(int op, int64_t M, int64_t in_features, int64_t out_
     case QLORA_OP_LINEAR_BWD_DROPOUT:
       if (M < 1 || r < 1) return 0;
       return bwd_ws(M, in_features, out_features, r).total;
+    case QLORA_OP_LINEAR_FWD_SLOTS:
+      if (M < 1 || r < 1) return 0;
+      return slots_ws(M, r);
     default:
       return static_cast<size_t>(-1);
   }
@@ -1296,6 +1421,39 @@ int qlora_linear_bwd_group(int n, const qlora_linear_problem* problems, void* wo
     }
     return rc;
   });
+}
+
+int qlora_token_slots(const int32_t* lengths, const int32_t* slots, int64_t n_requests, int64_t n_tokens,
+                      int32_t* ids, void* stream) {
+  if (n_requests < 0 || n_tokens < 0) return QLORA_ERR_INVALID_ARG;
+  if (n_requests > 0 && (!lengths || !slots || !aligned(lengths, 4) || !aligned(slots, 4)))
+    return QLORA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!ids || !aligned(ids, 4))) return QLORA_ERR_INVALID_ARG;
+  if (n_tokens > kMaxTokens || n_requests > kMaxTokens) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (n_tokens == 0) return QLORA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  {
+    LaunchTimer lt_("token_slots", st);
+    qnf4::token_slots_kernel<<<static_cast<unsigned>(cdiv(n_tokens, qnf4::kTsTile)), qnf4::kTsThreads, 0, st>>>(
+        lengths, slots, n_requests, n_tokens, ids);
+  }
+  QLORA_CUDA_TRY(cudaGetLastError());
+  return QLORA_OK;
+}
+
+int qlora_linear_fwd_slots(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, const uint16_t* A,
+                           const uint16_t* B, int64_t n_adapters, int r, const float* scale, const int32_t* ids,
+                           uint16_t* h, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x || !weight_ok(w) || !A || !B || !scale || !ids || !h) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(h, 16) || !aligned(scale, 4) ||
+      !aligned(ids, 4))
+    return QLORA_ERR_INVALID_ARG;
+  const int sc = check_linear_shapes(M, w, r);
+  if (sc != QLORA_OK) return sc;
+  if (n_adapters < 1 || n_adapters * r > kMaxTokens) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < slots_ws(M, r)) return QLORA_ERR_WORKSPACE;
+  return linear_fwd_slots_impl(x, M, w, A, B, n_adapters, r, scale, ids, h, workspace,
+                               static_cast<cudaStream_t>(stream));
 }
 
 int qlora_last_device_status(void* stream) {

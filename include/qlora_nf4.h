@@ -77,7 +77,8 @@ enum {
   QLORA_OP_LINEAR_FWD = 2,
   QLORA_OP_LINEAR_BWD = 3,
   QLORA_OP_LINEAR_FWD_DROPOUT = 4,
-  QLORA_OP_LINEAR_BWD_DROPOUT = 5
+  QLORA_OP_LINEAR_BWD_DROPOUT = 5,
+  QLORA_OP_LINEAR_FWD_SLOTS = 6
 };
 
 /* A quantized weight: device pointers in the format described above. */
@@ -384,6 +385,47 @@ int qlora_linear_bwd_group(int n, const qlora_linear_problem* problems, void* wo
                            void* stream);
 
 /*
+ * One adapter per request.  A server keeps n_adapters adapters of one base in
+ * a table (a "slot" each) and runs the tokens of many requests in one call.
+ *
+ * qlora_token_slots -- the slot of every token, from the requests' lengths.
+ *   The requests' tokens lie one after another; ids[t] is slots[k] of the
+ *   request k that holds token t, and -1 for the tokens behind the last
+ *   request.  Lengths may be zero (negative ones count as zero) and may add
+ *   up to more than n_tokens (the rest is cut off); slots are copied as they
+ *   are.  One map serves every projection of a step.
+ *   lengths, slots  device int32 [n_requests] (unused when n_requests = 0)
+ *   ids             device int32 [n_tokens] (written)
+ *   These three need 4-byte alignment only.
+ *
+ * qlora_linear_fwd_slots -- the layer with the adapter of each token's slot:
+ *   h[m] = W0 x[m] + us[m] B_a^T,  us[m] = bf16(scale[a] * A_a x[m]),
+ *   a = ids[m]
+ * ("QLoRA", llm-compass, 方法与公式, the displayed formula, per token;
+ * skillbyai, Merging the adapter for serving: an unmerged adapter can be
+ * swapped over one base).  A token whose slot is outside [0, n_adapters)
+ * gets the base product alone.
+ *   x        device bf16 [M, in]
+ *   w        quantized W0, rows = out, cols = in
+ *   A        device bf16 [n_adapters, r, in]
+ *   B        device bf16 [n_adapters, out, r]
+ *            (an adapter of lower rank is stored with zero rows and columns)
+ *   scale    device fp32 [n_adapters], alpha / r of each adapter, with its
+ *            own rank; 4-byte aligned
+ *   ids      device int32 [M], 4-byte aligned, in any order
+ *   h        device bf16 [M, out] (written)
+ * workspace: qlora_workspace_size(QLORA_OP_LINEAR_FWD_SLOTS, M, in, out, r).
+ * Size rules: those of qlora_linear_fwd, and n_adapters >= 1 with
+ * n_adapters * r < 2^31 - 1024.  The adapters' values outside the slots in
+ * use are not read into any result.
+ */
+int qlora_token_slots(const int32_t* lengths, const int32_t* slots, int64_t n_requests, int64_t n_tokens,
+                      int32_t* ids, void* stream);
+int qlora_linear_fwd_slots(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, const uint16_t* A,
+                           const uint16_t* B, int64_t n_adapters, int r, const float* scale, const int32_t* ids,
+                           uint16_t* h, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * qlora_last_device_status -- synchronizes `stream`, then reads and clears
  * the current device's error flag.  Kernels that wait on another part of the
  * device (pipeline barriers inside the GEMMs) give up after a bounded time
@@ -418,7 +460,8 @@ int qlora_selftest_wait_timeout(void* stream);
  * the number of launches since the last reset.  Names: "quantize_blocks",
  * "scale_mean_tree", "dq_scales", "dequantize", "gemm_fwd", "gemm_dx",
  * "gemv", "gemv_finalize", "lora_rowwise" (us), "lora_rowwise_du" (du),
- * "lora_colwise" (dA and dB), "merge_adapter", "dropout_dx".  Events are created by the library on first use (host-side
+ * "lora_colwise" (dA and dB), "merge_adapter", "dropout_dx", "token_slots",
+ * "slots_us", "slots_gemm".  Events are created by the library on first use (host-side
  * CUDA objects, no device memory).  Not for use during stream capture.
  *
  * qlora_timing_enable: on != 0 enables, 0 disables; returns the previous state.
