@@ -192,6 +192,22 @@ bool make_tmap_codes(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t 
   return r == CUDA_SUCCESS;
 }
 
+// 2-D bf16 row-major [rows, cols] tensor (cols % 64 == 0) seen as [cols / 64][rows][64], box {64, box_rows, box_blocks}:
+// several 64-wide K blocks of a row tile in one copy, each a 128-byte-swizzled tile.
+bool make_tmap_bf16_blocks(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                           uint32_t box_blocks) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {64, rows, cols / 64};
+  cuuint64_t strides[2] = {cols * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, box_blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Per-device facts the launch planning needs on every call, looked up once
 // per device (a failed lookup, e.g. with no device, is not cached).
 constexpr int kMaxDevices = 64;
@@ -936,6 +952,7 @@ int slots_gemm_clusters(int ks) {
   const int c = cache[dev][ks].load(std::memory_order_relaxed);
   if (c > 0) return c;
   const int smem = qnf4::sg_smem_bytes(qnf4::kSgMaxN);
+  const auto kern = qnf4::slots_gemm_kernel<2, 2>;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(1, static_cast<unsigned>(ks), 1);
   cfg.blockDim = dim3(qnf4::kSgThreads);
@@ -948,8 +965,8 @@ int slots_gemm_clusters(int ks) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (set_max_smem(reinterpret_cast<const void*>(qnf4::slots_gemm_kernel), smem) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, qnf4::slots_gemm_kernel, &cfg) != cudaSuccess || n < 1) {
+  if (set_max_smem(reinterpret_cast<const void*>(kern), smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
     (void)cudaGetLastError();
     return std::max(1, device_sm_count() / ks);
   }
@@ -1004,11 +1021,15 @@ int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* 
   a.timeout_ns = g_timeout_ns.load();
   CUtensorMap tm_codes, tm_x;
   if (!make_tmap_codes(&tm_codes, w->codes, static_cast<uint64_t>(out), static_cast<uint64_t>(in / 2), qnf4::kSgRows) ||
-      !make_tmap_bf16(&tm_x, x, static_cast<uint64_t>(M), static_cast<uint64_t>(in), static_cast<uint32_t>(N)))
+      !make_tmap_bf16_blocks(&tm_x, x, static_cast<uint64_t>(M), static_cast<uint64_t>(in), static_cast<uint32_t>(N),
+                             static_cast<uint32_t>(qnf4::sg_kb(N))))
     return QLORA_ERR_CUDA;
   const int ks = slots_gemm_split(tiles, static_cast<int>(cdiv(in, 256)));
   const int smem = qnf4::sg_smem_bytes(N);
-  QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(qnf4::slots_gemm_kernel), smem));
+  const auto kern = qnf4::sg_kb(N) == 2      ? qnf4::slots_gemm_kernel<2, 2>
+                    : qnf4::sg_stages(N) == 2 ? qnf4::slots_gemm_kernel<4, 2>
+                                              : qnf4::slots_gemm_kernel<4, 4>;
+  QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), smem));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(ks), 1);
   cfg.blockDim = dim3(qnf4::kSgThreads);
@@ -1023,7 +1044,7 @@ int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* 
   cfg.numAttrs = ks > 1 ? 1 : 0;
   {
     LaunchTimer lt_("slots_gemm", st);
-    QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, qnf4::slots_gemm_kernel, tm_codes, tm_x, a));
+    QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, tm_codes, tm_x, a));
   }
   QLORA_CUDA_TRY(cudaGetLastError());
   return QLORA_OK;
