@@ -929,124 +929,101 @@ int check_bwd_args(const uint16_t* dh, const uint16_t* x, const uint16_t* us, in
 }
 
 // ------------------------------------------------------------------ one adapter per request
-// Workspace of linear_fwd_slots: us [M, r8] bf16.
-size_t slots_ws(int64_t M, int r) { return round256(static_cast<size_t>(M) * padded_rank(r) * 2); }
+// Workspace of linear_fwd_slots: us [M, r8] bf16, the row tiles' tickets, the
+// fp32 partials of tiles cut between CTAs (one launch's, reused by the next).
+struct SlotsWs {
+  size_t ticket_off, part_off, total;
+};
+
+// Tokens of one launch: equal shares of at most 256.
+int64_t slots_launch_tokens(int64_t M) { return cdiv(M, cdiv(M, qnf4::kSgMaxN)); }
+
+int slots_ctas(int64_t in, int64_t out) {
+  const int64_t units = cdiv(out, qnf4::kSgRows) * cdiv(in, 256);
+  return static_cast<int>(std::min<int64_t>({device_sm_count(), qnf4::kSgMaxCtas, units}));
+}
+
+SlotsWs slots_ws(int64_t M, int64_t in, int64_t out, int r) {
+  SlotsWs w{};
+  w.ticket_off = round256(static_cast<size_t>(M) * padded_rank(r) * 2);
+  w.part_off = w.ticket_off + round256(static_cast<size_t>(cdiv(out, qnf4::kSgRows)) * 4);
+  const size_t N = static_cast<size_t>(cdiv(slots_launch_tokens(M), 16) * 16);
+  w.total = w.part_off + static_cast<size_t>(slots_ctas(in, out)) * 2 * N * qnf4::kSgRows * 4;
+  return w;
+}
 
 int launch_slots_us(const uint16_t* x, const uint16_t* A, const float* scale, const int32_t* ids, int64_t M,
-                    int64_t in, int64_t n_adapters, int r, uint16_t* us, cudaStream_t st) {
+                    int64_t in, int64_t n_adapters, int r, uint16_t* us, uint32_t* tickets, int n_tickets,
+                    cudaStream_t st) {
   const int r8 = padded_rank(r);
   {
     LaunchTimer lt_("slots_us", st);
-    qnf4::slots_us_kernel<<<static_cast<unsigned>(cdiv(M * (r8 / 8), 8)), 256, 0, st>>>(x, A, scale, ids, M, in,
-                                                                                      n_adapters, r, r8, us);
+    qnf4::slots_us_kernel<<<static_cast<unsigned>(M * (r8 / qnf4::kUsRanks)), qnf4::kUsThreads, 0, st>>>(
+        x, A, scale, ids, in, n_adapters, r, r8, us, tickets, n_tickets);
   }
   QLORA_CUDA_TRY(cudaGetLastError());
   return QLORA_OK;
-}
-
-// Clusters of ks CTAs of the kernel that the device holds at once, looked up
-// once per device (at the largest shared-memory size; one CTA per SM at any).
-int slots_gemm_clusters(int ks) {
-  static std::atomic<int> cache[kMaxDevices][9];
-  const int dev = current_device();
-  const int c = cache[dev][ks].load(std::memory_order_relaxed);
-  if (c > 0) return c;
-  const int smem = qnf4::sg_smem_bytes(qnf4::kSgMaxN);
-  const auto kern = qnf4::slots_gemm_kernel<2, 2>;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(1, static_cast<unsigned>(ks), 1);
-  cfg.blockDim = dim3(qnf4::kSgThreads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = static_cast<unsigned>(ks);
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (set_max_smem(reinterpret_cast<const void*>(kern), smem) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-    (void)cudaGetLastError();
-    return std::max(1, device_sm_count() / ks);
-  }
-  cache[dev][ks].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-// Split of the K axis: the cluster size whose rounds of clusters, each of
-// (units per CTA + the fixed cost of a CTA in units), come out shortest.
-int slots_gemm_split(int64_t tiles, int n_units) {
-  constexpr int kFixed = 4;                    // prologue, epilogue and reduction, in 256-column units
-  int best = 1;
-  int64_t best_cost = 0;
-  for (int ks = 1; ks <= 8 && ks <= n_units; ++ks) {
-    const int64_t cost = cdiv(tiles, slots_gemm_clusters(ks)) * (cdiv(n_units, ks) + kFixed);
-    if (ks == 1 || cost < best_cost) {
-      best = ks;
-      best_cost = cost;
-    }
-  }
-  return best;
 }
 
 int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, const uint16_t* A,
                           const uint16_t* B, int64_t n_adapters, int r, const float* scale, const int32_t* ids,
                           uint16_t* h, void* workspace, cudaStream_t st) {
   const int64_t in = w->cols, out = w->rows;
-  uint16_t* us = static_cast<uint16_t*>(workspace);
-  const int rc = launch_slots_us(x, A, scale, ids, M, in, n_adapters, r, us, st);
-  if (rc != QLORA_OK) return rc;
-  // equal token tiles of at most 256, in whole UMMA steps of 16
-  const int64_t tok_tiles = cdiv(M, qnf4::kSgMaxN);
-  const int N = static_cast<int>(cdiv(cdiv(M, tok_tiles), 16) * 16);
-  const int64_t tiles = cdiv(out, qnf4::kSgRows) * tok_tiles;
-  if (tiles > kMaxTokens) return QLORA_ERR_UNSUPPORTED_SHAPE;
-  qnf4::SlotsGemmArgs a{};
-  a.q8 = w->q8;
-  a.step2 = w->step2;
-  a.mean = w->mean;
-  a.us = us;
-  a.B = B;
-  a.ids = ids;
-  a.h = h;
-  a.n_adapters = n_adapters;
-  a.M = static_cast<int>(M);
-  a.out = static_cast<int>(out);
-  a.K = static_cast<int>(in);
-  a.r = r;
-  a.r8 = padded_rank(r);
-  a.N = N;
-  a.L = tables().L;
-  a.timeout_ns = g_timeout_ns.load();
-  CUtensorMap tm_codes, tm_x;
-  if (!make_tmap_codes(&tm_codes, w->codes, static_cast<uint64_t>(out), static_cast<uint64_t>(in / 2), qnf4::kSgRows) ||
-      !make_tmap_bf16_blocks(&tm_x, x, static_cast<uint64_t>(M), static_cast<uint64_t>(in), static_cast<uint32_t>(N),
-                             static_cast<uint32_t>(qnf4::sg_kb(N))))
+  const SlotsWs ws = slots_ws(M, in, out, r);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  uint16_t* us = reinterpret_cast<uint16_t*>(base);
+  uint32_t* tickets = reinterpret_cast<uint32_t*>(base + ws.ticket_off);
+  const int row_tiles = static_cast<int>(cdiv(out, qnf4::kSgRows));
+  const int r8 = padded_rank(r);
+  const int64_t step = slots_launch_tokens(M);
+  CUtensorMap tm_codes;
+  if (!make_tmap_codes(&tm_codes, w->codes, static_cast<uint64_t>(out), static_cast<uint64_t>(in / 2), qnf4::kSgRows))
     return QLORA_ERR_CUDA;
-  const int ks = slots_gemm_split(tiles, static_cast<int>(cdiv(in, 256)));
-  const int smem = qnf4::sg_smem_bytes(N);
-  const auto kern = qnf4::sg_kb(N) == 2      ? qnf4::slots_gemm_kernel<2, 2>
-                    : qnf4::sg_stages(N) == 2 ? qnf4::slots_gemm_kernel<4, 2>
-                                              : qnf4::slots_gemm_kernel<4, 4>;
-  QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), smem));
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(ks), 1);
-  cfg.blockDim = dim3(qnf4::kSgThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = static_cast<unsigned>(ks);
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = ks > 1 ? 1 : 0;
-  {
-    LaunchTimer lt_("slots_gemm", st);
-    QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, tm_codes, tm_x, a));
+  for (int64_t m0 = 0; m0 < M; m0 += step) {
+    const int64_t m = std::min(step, M - m0);
+    const int rc = launch_slots_us(x + m0 * in, A, scale, ids + m0, m, in, n_adapters, r, us + m0 * r8, tickets,
+                                   row_tiles, st);
+    if (rc != QLORA_OK) return rc;
+    qnf4::SlotsGemmArgs a{};
+    a.q8 = w->q8;
+    a.step2 = w->step2;
+    a.mean = w->mean;
+    a.us = us + m0 * r8;
+    a.B = B;
+    a.ids = ids + m0;
+    a.h = h + m0 * out;
+    a.part = reinterpret_cast<float*>(base + ws.part_off);
+    a.tickets = tickets;
+    a.n_adapters = n_adapters;
+    a.M = static_cast<int>(m);
+    a.out = static_cast<int>(out);
+    a.K = static_cast<int>(in);
+    a.r = r;
+    a.r8 = r8;
+    a.N = static_cast<int>(cdiv(m, 16) * 16);
+    a.L = tables().L;
+    a.timeout_ns = g_timeout_ns.load();
+    CUtensorMap tm_x;
+    if (!make_tmap_bf16_blocks(&tm_x, x + m0 * in, static_cast<uint64_t>(m), static_cast<uint64_t>(in),
+                               static_cast<uint32_t>(a.N), static_cast<uint32_t>(qnf4::sg_kb(a.N))))
+      return QLORA_ERR_CUDA;
+    const auto kern = a.N <= 32    ? qnf4::slots_gemm_kernel<4, 4, true>
+                      : a.N <= 64  ? qnf4::slots_gemm_kernel<4, 2, true>
+                      : a.N <= 128 ? qnf4::slots_gemm_kernel<2, 2, true>
+                                   : qnf4::slots_gemm_kernel<2, 2, false>;
+    const int smem = qnf4::sg_smem_bytes(a.N);
+    QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), smem));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(slots_ctas(in, out)));
+    cfg.blockDim = dim3(qnf4::kSgThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    {
+      LaunchTimer lt_("slots_gemm", st);
+      QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, tm_codes, tm_x, a));
+    }
+    QLORA_CUDA_TRY(cudaGetLastError());
   }
-  QLORA_CUDA_TRY(cudaGetLastError());
   return QLORA_OK;
 }
 
@@ -1115,8 +1092,8 @@ size_t qlora_workspace_size(int op, int64_t M, int64_t in_features, int64_t out_
       if (M < 1 || r < 1) return 0;
       return bwd_ws(M, in_features, out_features, r).total;
     case QLORA_OP_LINEAR_FWD_SLOTS:
-      if (M < 1 || r < 1) return 0;
-      return slots_ws(M, r);
+      if (M < 1 || r < 1 || in_features < 64 || out_features < 64) return 0;
+      return slots_ws(M, in_features, out_features, r).total;
     default:
       return static_cast<size_t>(-1);
   }
@@ -1472,7 +1449,8 @@ int qlora_linear_fwd_slots(const uint16_t* x, int64_t M, const qlora_nf4_weight*
   const int sc = check_linear_shapes(M, w, r);
   if (sc != QLORA_OK) return sc;
   if (n_adapters < 1 || n_adapters * r > kMaxTokens) return QLORA_ERR_UNSUPPORTED_SHAPE;
-  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < slots_ws(M, r)) return QLORA_ERR_WORKSPACE;
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < slots_ws(M, w->cols, w->rows, r).total)
+    return QLORA_ERR_WORKSPACE;
   return linear_fwd_slots_impl(x, M, w, A, B, n_adapters, r, scale, ids, h, workspace,
                                static_cast<cudaStream_t>(stream));
 }

@@ -11,28 +11,38 @@
 // 32 tensor-memory columns that the UMMA reads as its A operand, and x comes
 // as the B operand through TMA.
 //
-// The adapters ride along as extra K stages.  The CTA lists the distinct
-// adapters of its token tile (first appearance first); the rank columns of
-// the listed adapters, one after another, form a K axis that is cut into
-// stages: the A operand is B_a[n][j], the B operand us[m][j] where token m
-// uses that adapter and zero elsewhere.
+// The adapters ride along as extra K.  The CTA lists the distinct adapters of
+// the tokens (first appearance first); the rank columns of the listed
+// adapters, one after another, form a K axis behind that of the base: the A
+// operand is B_a[n][j], the B operand us[m][j] where token m uses that adapter
+// and zero elsewhere.  A B value that is infinite or NaN would reach the other
+// tokens through their zeros, so it is carried as 0 and the tile is marked;
+// the epilogue then adds those products to the adapter's own tokens.
 //
-// A B value that is infinite or NaN would reach the other tokens of the tile
-// through their zeros, so the stages carry 0 in its place and the tile is
-// marked; the epilogue then adds those products to the adapter's own tokens.
+// Schedule: K is cut into units of 256; the units of all row tiles, tile after
+// tile, are dealt out evenly to a persistent grid of one CTA per SM, so every
+// CTA streams the same amount whatever the shape.  A tile that one CTA holds
+// goes straight to h; of a tile cut between CTAs each leaves an fp32 partial,
+// and the one that finishes last (a ticket per tile) adds them in CTA order,
+// so the result does not depend on which CTA ran when.  (Rounds of whole
+// tiles, split over clusters, lost a quarter to the last round and paid a
+// prologue per round: 125 us for the 70B up projection at 16 tokens.)
 //
-// The K axis is split over the CTAs of a cluster (256-column units of the
-// base, and the adapter stages, each evenly); the fp32 partial tiles are
-// added over distributed shared memory in rank order (deterministic).
+// Decode.  The integer pipe (64 lanes per clock) bounds a decode by byte
+// permutes, about 4 operations per weight.  Up to 128 tokens there is room
+// for a 64 KB table instead, for every byte of two codes the two fp32 levels,
+// one copy per lane: a pair of weights takes one prmt (the address), one
+// 8-byte shared load, one packed fp32 multiply and one conversion, and every
+// weight is bf16(level * scale) as everywhere else.
 //
-// Roles per CTA (8 + 4 G warps):
+// Roles per CTA (24 warps):
 //   warp 0        TMA of the x tiles (one copy per stage)
 //   warp 1        TMEM allocation; UMMA issue
-//   warp 2        TMA of the code tiles (128 rows x 128 bytes: 256 K columns)
+//   warp 2        TMA of the code tiles (128 rows x 128 bytes: one unit)
 //   warps 4-7     block scales of each code tile (one row per thread)
-//   warps 8-23    four dequant groups of 4 warps, group g takes the 64-wide
-//                 K blocks g, g + 4, ..
-// A stage is KB = 4 blocks of K (2 above 128 tokens, where two stages of x
+//   warps 8-23    four dequant groups of 4 warps, group g takes the g-th
+//                 64-wide block of every unit; then the epilogue
+// A stage is KB = 4 blocks of K (2 above 64 tokens, where two stages of x
 // would not fit otherwise).  The issuing warp runs its loop as a whole, with
 // one elected lane inside the instruction: its operands then stay uniform and
 // an UMMA of 16 tokens issues in 10 clocks; from a one-lane branch it took 118.
@@ -43,38 +53,38 @@
 
 namespace qnf4 {
 
-constexpr int kSgRows = 128;                  // weight rows per CTA
-constexpr int kSgMaxN = 256;                  // tokens per CTA
-constexpr int kSgUnits = 4;                   // code tiles in flight
+constexpr int kSgRows = 128;                  // weight rows per tile
+constexpr int kSgMaxN = 256;                  // tokens per launch
+constexpr int kSgMaxCtas = 256;
+constexpr int kSgUnits = 3;                   // code tiles in flight
 constexpr int kSgCodeTile = kSgRows * 128;    // 16 KB: 256 K columns
-constexpr int kSgABlock = kSgRows * 128;      // 16 KB: one 64-wide block of the A operand
 constexpr int kSgABlocks = 8;                 // blocks of the tensor-memory A ring, 32 columns each
 constexpr uint32_t kSgAccCol = 256;           // the accumulator, behind the A ring
+constexpr uint32_t kSgTmemCols = 512;
 constexpr int kSgMaxStages = 4;
 constexpr int kSgGroups = 4;                  // dequant groups
-constexpr int kSgThreads = (8 + 4 * kSgGroups) * 32;
+constexpr int kSgDecThreads = kSgGroups * 128;
+constexpr int kSgThreads = 256 + kSgDecThreads;
 
-// K blocks per stage, and x stages in flight (at most 64 KB).
-__host__ __device__ constexpr int sg_kb(int N) { return N <= 128 ? 4 : 2; }
-__host__ __device__ constexpr int sg_stages(int N) { return N <= 64 ? 4 : 2; }
-__host__ __device__ constexpr int sg_x_bytes(int N) { return sg_stages(N) * sg_kb(N) * N * 128; }
-__host__ __device__ constexpr int sg_list_bytes() { return 2 * kSgMaxN * 4 + 64; }
-// The fp32 partial tile lies over the rings once they are done with.
-__host__ __device__ constexpr int sg_ring_bytes(int N) {
-  return sg_x_bytes(N) + kSgUnits * kSgCodeTile;
+// K blocks per stage, x stages in flight (64 KB, without the table 128 KB).
+__host__ __device__ constexpr int sg_kb(int N) { return N <= 64 ? 4 : 2; }
+__host__ __device__ constexpr int sg_stages(int N) { return N <= 32 ? 4 : 2; }
+__host__ __device__ constexpr bool sg_lut(int N) { return N <= 128; }
+// Shared memory by absolute shared address: the level table sits on a 64 KB
+// boundary (prmt assembles its addresses), x behind it; codes, scales, lists
+// and barriers before it.  Without the table x starts at the boundary.
+constexpr uint32_t kSgTableAt = 0x10000;
+__host__ __device__ constexpr int sg_low_bytes() {
+  return kSgUnits * (kSgCodeTile + kSgRows * 16) + 2 * kSgMaxN * 4 + kSgMaxCtas * 4 + 64 + 512;
 }
-// At least kSgMinSmem, so that no other CTA of this library that allocates
-// tensor memory fits beside this one (the rank-r kernels take 72 KB or more):
-// two CTAs that wait for each other's tensor memory while both wait for their
-// clusters could not finish.
-constexpr int kSgMinSmem = 160 * 1024;
-__host__ __device__ constexpr int sg_smem_bytes(int N) {
-  const int need = sg_ring_bytes(N) + kSgUnits * kSgRows * 16 + sg_list_bytes() + 512 + 1024;
-  return need > kSgMinSmem ? need : kSgMinSmem;
+__host__ __device__ constexpr int sg_smem_bytes(int N) {   // (the window starts at or above address 0)
+  return static_cast<int>(kSgTableAt) + (sg_lut(N) ? 65536 + sg_stages(N) * sg_kb(N) * N * 128 : 131072);
 }
-static_assert(kSgMaxN * kSgRows * 4 <= sg_ring_bytes(kSgMaxN) && 16 * kSgRows * 4 <= sg_ring_bytes(16),
-              "the partial tile fits the rings");
-__host__ __device__ constexpr int sg_tmem_cols(int) { return 512; }
+static_assert(sg_low_bytes() + 1024 + 1024 <= static_cast<int>(kSgTableAt), "the low part fits below the table");
+static_assert(sg_smem_bytes(kSgMaxN) <= 227 * 1024 && sg_smem_bytes(128) <= 227 * 1024, "shared memory of a CTA");
+// No other CTA of this library that allocates tensor memory fits beside this
+// one (the rank-r kernels take 72 KB or more).
+static_assert(sg_smem_bytes(16) > (228 - 72) * 1024, "one CTA with tensor memory per SM");
 
 struct SlotsGemmArgs {
   const int8_t* q8;
@@ -84,9 +94,11 @@ struct SlotsGemmArgs {
   const uint16_t* B;        // [n_adapters, out, r]
   const int32_t* ids;       // [M]
   uint16_t* h;              // [M, out]
+  float* part;              // [2 * CTAs][N][128]: a CTA's first and last tile, where cut
+  uint32_t* tickets;        // [row tiles], zero before the launch
   int64_t n_adapters;
-  int M, out, K, r, r8;
-  int N;                    // tokens per tile (a multiple of 16)
+  int M, out, K, r, r8;     // M <= 256
+  int N;                    // M rounded up to 16
   Levels L;
   uint64_t timeout_ns;
 };
@@ -164,25 +176,45 @@ __device__ __forceinline__ void lds_v4(uint32_t addr, uint32_t (&v)[4]) {
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
 
-// KB, S: sg_kb(N), sg_stages(N).
-template <int KB, int S>
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The products of an adapter row's infinite or NaN B values with a token's us.
+__device__ __noinline__ float slots_odd_term(const uint16_t* B_row, const uint16_t* us, int r) {
+  float f = 0.f;
+  for (int j = 0; j < r; ++j) {
+    const uint32_t b = __ldg(B_row + j);
+    if ((b & 0x7F80u) == 0x7F80u)
+      f = fmaf(__uint_as_float(static_cast<uint32_t>(us[j]) << 16), __uint_as_float(b << 16), f);
+  }
+  return f;
+}
+
+// First unit of CTA c when T units are dealt out to G CTAs.
+__device__ __forceinline__ int64_t sg_unit_begin(int64_t c, int64_t T, int64_t G) { return T * c / G; }
+
+// KB, S, kLut: sg_kb(N), sg_stages(N), sg_lut(N).
+template <int KB, int S, bool kLut>
 __global__ void __launch_bounds__(kSgThreads, 1)
 slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_x,
                   const SlotsGemmArgs args) {
+  constexpr int SA = kSgABlocks / KB;                        // stages of the A ring
+  constexpr int SPU = 4 / KB;                                // stages per unit
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  uint8_t* low = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  uint8_t* table = smem_raw + (kSgTableAt - raw_addr);
   const int N = args.N;
-  constexpr int SA = kSgABlocks / KB;                            // stages of the A ring
   const int x_blk = N * 128, x_stage = KB * x_blk;
-  uint8_t* x_ring = smem;
-  uint8_t* c_ring = x_ring + S * x_stage;
+  uint8_t* c_ring = low;
   float* s_ring = reinterpret_cast<float*>(c_ring + kSgUnits * kSgCodeTile);   // [unit][block][row]
   int32_t* tok_id = reinterpret_cast<int32_t*>(s_ring + kSgUnits * kSgRows * 4);
   int32_t* list = tok_id + kSgMaxN;                          // distinct adapters, first appearance first
-  int32_t* counts = list + kSgMaxN;                          // [8] leaders per warp of 32 tokens
-  int32_t* odd = counts + 8;                                 // some B value of a stage was not finite
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tok_id) + sg_list_bytes());
+  int32_t* parts = list + kSgMaxN;                           // the partials of the tile being added up
+  int32_t* counts = parts + kSgMaxCtas;                      // [8] leaders per warp of 32 tokens
+  volatile int32_t* odd = counts + 8;                        // [2] by segment: a B value was not finite
+  volatile int32_t* last_flag = counts + 10;                 // [2] this CTA adds the tile up; some part was odd
+  uint8_t* x_ring = kLut ? table + 65536 : table;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(counts + 16);
   uint64_t* xfull = bars;                                    // the stage's x tile landed
   uint64_t* xempty = xfull + kSgMaxStages;                   // the UMMAs on the x tile finished
   uint64_t* afull = xempty + kSgMaxStages;                   // the stage's A operand is written
@@ -190,21 +222,16 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   uint64_t* cfull = aempty + kSgMaxStages;                   // the code tile landed
   uint64_t* sfull = cfull + kSgUnits;                        // its scales are written
   uint64_t* cempty = sfull + kSgUnits;                       // codes and scales are read
-  uint64_t* acc_full = cempty + kSgUnits;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
+  uint64_t* acc_full = cempty + kSgUnits;                    // a segment's accumulator is complete
+  uint64_t* acc_empty = acc_full + 1;                        // and read
+  uint64_t* dec_bar = acc_empty + 1;                         // the dequant warps among themselves
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dec_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row_tiles = (args.out + kSgRows - 1) / kSgRows;
-  const int n0 = (static_cast<int>(blockIdx.x) % row_tiles) * kSgRows;
-  const int m0 = (static_cast<int>(blockIdx.x) / row_tiles) * N;
-  const int ks = static_cast<int>(gridDim.y), split = static_cast<int>(blockIdx.y);
   const uint64_t tmo = args.timeout_ns;
   const int n_blk = args.K / 64;
-  const int n_units = (n_blk + 3) / 4;
-  const int u_begin = static_cast<int>(static_cast<int64_t>(n_units) * split / ks);
-  const int u_end = static_cast<int>(static_cast<int64_t>(n_units) * (split + 1) / ks);
-  const int n_base = (u_end - u_begin) * 4 / KB;             // stages of the base; blocks past K are zero
+  const int UB = (n_blk + 3) / 4;                            // base units per tile
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSgMaxStages; ++s) {
@@ -219,56 +246,80 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       mbar_init(cempty + u, 16);                             // four blocks x four warps
     }
     mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 16);
+    mbar_init(dec_bar, 16);
     *abort_flag = 0;
-    *odd = 0;
+    odd[0] = odd[1] = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_codes);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, static_cast<uint32_t>(sg_tmem_cols(N)));
+    tmem_alloc(tmem_holder, kSgTmemCols);
     tmem_relinquish();
   }
-  // the token tile's slots; -1 for no adapter and for tokens past the batch
-  if (threadIdx.x < kSgMaxN) {
-    const int m = m0 + static_cast<int>(threadIdx.x);
-    int32_t a = -1;
-    if (static_cast<int>(threadIdx.x) < N && m < args.M) {
-      a = __ldg(args.ids + m);
-      if (a < 0 || a >= args.n_adapters) a = -1;
-    }
-    tok_id[threadIdx.x] = a;
-  }
-  __syncthreads();
+  // The tokens' slots, -1 for no adapter and for rows past the batch, and the
+  // distinct ones: a token leads if no token before it has its slot.
   bool leader = false;
+  int32_t my_id = -1;
   if (threadIdx.x < kSgMaxN) {                               // whole warps
     const int t = threadIdx.x;
-    const int32_t a = tok_id[t];
-    leader = a >= 0;
-    for (int i = 0; leader && i < t; ++i)
-      if (tok_id[i] == a) leader = false;
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, leader);
-    if (lane == 0) counts[warp] = __popc(b);
+    if (t < args.M) {
+      my_id = __ldg(args.ids + t);
+      if (my_id < 0 || my_id >= args.n_adapters) my_id = -1;
+    }
+    tok_id[t] = my_id;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, my_id);
+    leader = my_id >= 0 && (same & ((1u << lane) - 1u)) == 0;
+  }
+  if (kLut) {
+    // row b (256 bytes): lane l's copy of {level of the low code, level of the high code} at 8 l
+    for (int e = threadIdx.x; e < 256 * 16; e += kSgThreads) {
+      const int b = e >> 4;
+      float lo = 0.f, hi = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if ((b & 15) == j) lo = args.L.v[j];
+        if ((b >> 4) == j) hi = args.L.v[j];
+      }
+      *reinterpret_cast<float4*>(table + e * 16) = make_float4(lo, hi, lo, hi);
+    }
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  if (threadIdx.x < kSgMaxN) {
+    const int4* ids4 = reinterpret_cast<const int4*>(tok_id);
+    for (int i = 0; leader && i < warp * 8; ++i) {           // the warps before this one
+      const int4 o = ids4[i];
+      if (o.x == my_id || o.y == my_id || o.z == my_id || o.w == my_id) leader = false;
+    }
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, leader);
+    if (lane == 0) counts[warp] = __popc(b);
+  }
+  __syncthreads();
   int n_list = 0;
   {
     int before = 0;
 #pragma unroll
     for (int w = 0; w < kSgMaxN / 32; ++w) {
-      if (w < warp) before += counts[w];
-      n_list += counts[w];
+      const int c = counts[w];
+      if (w < warp) before += c;
+      n_list += c;
     }
     const uint32_t b = __ballot_sync(0xFFFFFFFFu, leader);
-    if (leader) list[before + __popc(b & ((1u << lane) - 1u))] = tok_id[threadIdx.x];
+    if (leader) list[before + __popc(b & ((1u << lane) - 1u))] = my_id;
   }
   __syncthreads();
   const uint32_t tmem_base = *tmem_holder;
   const int k_low = n_list * args.r8;                        // rank columns of the listed adapters
-  const int n_low_all = (k_low + 64 * KB - 1) / (64 * KB);   // adapter stages
-  const int l_begin = static_cast<int>(static_cast<int64_t>(n_low_all) * split / ks);
-  const int n_low = static_cast<int>(static_cast<int64_t>(n_low_all) * (split + 1) / ks) - l_begin;
-  const int n_it = n_base + n_low;
+  const int low_blk = (k_low + 63) / 64;
+  const int UPT = UB + (low_blk + 3) / 4;                    // units per tile
+  const int64_t G = gridDim.x;
+  const int64_t T = static_cast<int64_t>((args.out + kSgRows - 1) / kSgRows) * UPT;
+  const int64_t g0 = sg_unit_begin(blockIdx.x, T, G);
+  const int n_u = static_cast<int>(sg_unit_begin(blockIdx.x + 1, T, G) - g0);   // this CTA's units
+  const int tile0 = static_cast<int>(g0 / UPT), uu0 = static_cast<int>(g0 % UPT);
 
   // Bounded wait; false once it, or any other wait of the CTA, ran out of time.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -291,18 +342,23 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   if (warp == 0) {
     // ------------------------------------------------------------ x tiles
     if (lane == 0) {
-      tma_prefetch_desc(&tm_x);
-      int issued = 0;
-      for (int it = 0; it < n_base; ++it) {
-        const int s = it % S;
-        if (!wait(xempty + s, ((it / S) & 1u) ^ 1u)) break;
-        mbar_arrive_expect_tx(xfull + s, static_cast<uint32_t>(x_stage));
-        tma_load_3d(smem_u32(x_ring + s * x_stage), &tm_x, xfull + s, 0, m0, 4 * u_begin + it * KB);
-        ++issued;
+      int it = 0, uu = uu0;
+      bool ok = true;
+      for (int i = 0; i < n_u && ok; ++i) {
+        for (int j = 0; j < SPU; ++j, ++it) {
+          const int s = it % S;
+          if (!(ok = wait(xempty + s, ((it / S) & 1u) ^ 1u))) break;
+          if (uu < UB) {
+            mbar_arrive_expect_tx(xfull + s, static_cast<uint32_t>(x_stage));
+            tma_load_3d(smem_u32(x_ring + s * x_stage), &tm_x, xfull + s, 0, 0, uu * 4 + j * KB);
+          } else {
+            mbar_arrive(xfull + s);                          // an adapter stage: the dequant groups fill it
+          }
+        }
+        if (++uu == UPT) uu = 0;
       }
-      // only the last S issued stages can still be in flight
-      for (int it = issued > S ? issued - S : 0; it < issued; ++it)
-        mbar_wait_bounded(xfull + (it % S), (it / S) & 1u, tmo);
+      // only the last S stages can still be in flight
+      for (int k = it > S ? it - S : 0; k < it; ++k) mbar_wait_bounded(xfull + (k % S), (k / S) & 1u, tmo);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ UMMA issuer
@@ -310,131 +366,194 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
     const uint64_t desc_x = umma_desc_sw128(smem_u32(x_ring), 16, 1024);
     const uint32_t hi = static_cast<uint32_t>(desc_x >> 32);
     const uint32_t x_lo = static_cast<uint32_t>(desc_x);
+    const uint32_t d = tmem_base + kSgAccCol;
     const uint32_t elected = elect_one();
     uint32_t acc = 0;
-    for (int it = 0; it < n_it; ++it) {
-      const int s = it % S, sa = it % SA;
-      int blocks;                                            // blocks that hold anything
-      if (it < n_base) {
-        blocks = min(KB, n_blk - 4 * u_begin - it * KB);
-        if (!wait_warp(xfull + s, (it / S) & 1u)) break;     // an adapter stage's x tile comes with its A operand
-      } else {
-        blocks = min(KB, (k_low + 63) / 64 - (l_begin + it - n_base) * KB);
-      }
-      if (!wait_warp(afull + sa, (it / SA) & 1u)) break;
-      tc_fence_after_sync();
-      uint32_t b = x_lo + ((s * x_stage) >> 4);
-      uint32_t a = tmem_base + sa * KB * 32;
+    int it = 0, uu = uu0, seg = 0;
+    bool ok = true;
+    for (int i = 0; i < n_u && ok; ++i) {
+      if (acc == 0 && seg > 0 && !(ok = wait_warp(acc_empty, (seg - 1) & 1u))) break;
+      for (int j = 0; j < SPU; ++j, ++it) {
+        const int s = it % S, sa = it % SA;
+        const int blocks = uu < UB ? n_blk - uu * 4 - j * KB : low_blk - (uu - UB) * 4 - j * KB;
+        if (!(ok = wait_warp(xfull + s, (it / S) & 1u) && wait_warp(afull + sa, (it / SA) & 1u))) break;
+        tc_fence_after_sync();
+        uint32_t b = x_lo + ((s * x_stage) >> 4);
+        uint32_t a = tmem_base + sa * KB * 32;
 #pragma unroll
-      for (int blk = 0; blk < KB; ++blk, b += x_blk >> 4, a += 32) {
-        if (blk >= blocks) break;
-        umma_bf16_ts(tmem_base + kSgAccCol, a, b, hi, idesc, acc, elected);
-        umma_bf16_ts(tmem_base + kSgAccCol, a + 8, b + 2, hi, idesc, 1u, elected);
-        umma_bf16_ts(tmem_base + kSgAccCol, a + 16, b + 4, hi, idesc, 1u, elected);
-        umma_bf16_ts(tmem_base + kSgAccCol, a + 24, b + 6, hi, idesc, 1u, elected);
-        acc = 1u;
+        for (int blk = 0; blk < KB; ++blk, b += x_blk >> 4, a += 32) {
+          if (blk >= blocks) break;
+          umma_bf16_ts(d, a, b, hi, idesc, acc, elected);
+          umma_bf16_ts(d, a + 8, b + 2, hi, idesc, 1u, elected);
+          umma_bf16_ts(d, a + 16, b + 4, hi, idesc, 1u, elected);
+          umma_bf16_ts(d, a + 24, b + 6, hi, idesc, 1u, elected);
+          acc = 1u;
+        }
+        umma_commit_elected(smem_u32(aempty + sa), elected);
+        umma_commit_elected(smem_u32(xempty + s), elected);
       }
-      umma_commit_elected(smem_u32(aempty + sa), elected);
-      umma_commit_elected(smem_u32(xempty + s), elected);
+      if (++uu == UPT || i == n_u - 1) {                     // the segment ends
+        uu = 0;
+        acc = 0;
+        ++seg;
+        umma_commit_elected(smem_u32(acc_full), elected);
+      }
     }
-    umma_commit_elected(smem_u32(acc_full), elected);
-    mbar_wait_bounded(acc_full, 0, tmo);
+    // every UMMA finished before the CTA may leave
+    if (ok) mbar_wait_bounded(acc_full, (seg - 1) & 1u, tmo);
+    else {
+      umma_commit_elected(smem_u32(acc_full), elected);
+      mbar_wait_bounded(acc_full, seg & 1u, tmo);
+    }
   } else if (warp == 2) {
     // ------------------------------------------------------------ code tiles
     if (lane == 0) {
-      tma_prefetch_desc(&tm_codes);
-      int issued = 0;
-      for (int u = 0; u < u_end - u_begin; ++u) {
-        const int s = u % kSgUnits;
-        if (!wait(cempty + s, ((u / kSgUnits) & 1u) ^ 1u)) break;
-        mbar_arrive_expect_tx(cfull + s, kSgCodeTile);
-        tma_load_2d(smem_u32(c_ring + s * kSgCodeTile), &tm_codes, cfull + s, (u_begin + u) * 128, n0);
-        ++issued;
+      int uu = uu0, tile = tile0, s = 0, issued = 0;
+      uint32_t ph = 1;
+      for (int i = 0; i < n_u; ++i) {
+        if (uu < UB) {
+          if (!wait(cempty + s, ph)) break;
+          mbar_arrive_expect_tx(cfull + s, kSgCodeTile);
+          tma_load_2d(smem_u32(c_ring + s * kSgCodeTile), &tm_codes, cfull + s, uu * 128, tile * kSgRows);
+          ++issued;
+          if (++s == kSgUnits) { s = 0; ph ^= 1u; }
+        }
+        if (++uu == UPT) { uu = 0; ++tile; }
       }
-      for (int u = issued > kSgUnits ? issued - kSgUnits : 0; u < issued; ++u)
-        mbar_wait_bounded(cfull + (u % kSgUnits), (u / kSgUnits) & 1u, tmo);
+      for (int k = issued > kSgUnits ? issued - kSgUnits : 0; k < issued; ++k)
+        mbar_wait_bounded(cfull + (k % kSgUnits), (k / kSgUnits) & 1u, tmo);
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ block scales
-    // Thread t owns weight row n0 + t: the four scales of each code tile,
-    // loaded two tiles ahead.
+    // Thread t owns row t of each tile: the four scales of each code tile,
+    // loaded two units ahead.
     const int t = threadIdx.x - 128;
-    const int64_t row_blk = static_cast<int64_t>(n0 + t) * n_blk;
-    const bool row_ok = n0 + t < args.out;
     const float mu = __ldg(args.mean);
-    const bool word = (n_blk & 3) == 0;                      // a tile's four codes are one aligned word
+    const bool word = (n_blk & 3) == 0;                      // a unit's four codes are one aligned word
     struct In { uint32_t q; float s0, s3; };
-    auto load = [&](int u, In& d) {
-      if (!row_ok || u >= u_end) return;
-      const int64_t i = row_blk + 4 * u;
-      const int last = min(3, n_blk - 1 - 4 * u);
-      if (word) {
-        d.q = __ldg(reinterpret_cast<const uint32_t*>(args.q8 + i));
-      } else {
-        d.q = 0;
-        for (int b = 0; b <= last; ++b) d.q |= static_cast<uint32_t>(static_cast<uint8_t>(__ldg(args.q8 + i + b))) << (8 * b);
+    int l_uu = uu0, l_tile = tile0, l_i = 0;                 // the next unit to load
+    auto load = [&](In& d) {
+      if (l_i++ >= n_u) return;
+      const int row = l_tile * kSgRows + t;
+      if (l_uu < UB && row < args.out) {
+        const int64_t i = static_cast<int64_t>(row) * n_blk + 4 * l_uu;
+        const int last = min(3, n_blk - 1 - 4 * l_uu);
+        if (word) {
+          d.q = __ldg(reinterpret_cast<const uint32_t*>(args.q8 + i));
+        } else {
+          d.q = 0;
+          for (int b = 0; b <= last; ++b)
+            d.q |= static_cast<uint32_t>(static_cast<uint8_t>(__ldg(args.q8 + i + b))) << (8 * b);
+        }
+        d.s0 = __ldg(args.step2 + i / 256);
+        d.s3 = __ldg(args.step2 + (i + last) / 256);
       }
-      d.s0 = __ldg(args.step2 + i / 256);
-      d.s3 = __ldg(args.step2 + (i + last) / 256);
+      if (++l_uu == UPT) { l_uu = 0; ++l_tile; }
     };
     In a{}, b{};
-    load(u_begin, a);
-    load(u_begin + 1, b);
-    for (int u = u_begin; u < u_end; ++u) {
+    load(a);
+    load(b);
+    int uu = uu0, tile = tile0, s = 0;
+    uint32_t ph = 1;
+    for (int i = 0; i < n_u; ++i) {
       const In cur = a;
       a = b;
-      load(u + 2, b);
-      const int k = u - u_begin, s = k % kSgUnits;
-      if (!wait_warp(cempty + s, ((k / kSgUnits) & 1u) ^ 1u)) break;
-      const int64_t i = row_blk + 4 * u;
+      load(b);
+      if (uu < UB) {
+        if (!wait_warp(cempty + s, ph)) break;
+        const int row = tile * kSgRows + t;
+        const int64_t idx = static_cast<int64_t>(row) * n_blk + 4 * uu;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float st = ((i + e) / 256 == i / 256) ? cur.s0 : cur.s3;
-        const int q = static_cast<int8_t>(cur.q >> (8 * e));
-        s_ring[(s * 4 + e) * kSgRows + t] = row_ok && 4 * u + e < n_blk ? block_scale(q, st, mu) : 0.f;
+        for (int e = 0; e < 4; ++e) {
+          const float st = ((idx + e) / 256 == idx / 256) ? cur.s0 : cur.s3;
+          const int q = static_cast<int8_t>(cur.q >> (8 * e));
+          s_ring[(s * 4 + e) * kSgRows + t] = row < args.out && 4 * uu + e < n_blk ? block_scale(q, st, mu) : 0.f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfull + s);
+        if (++s == kSgUnits) { s = 0; ph ^= 1u; }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sfull + s);
+      if (++uu == UPT) { uu = 0; ++tile; }
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ dequant groups
     const int g = (warp - 8) >> 2;
     const int quad = warp & 3;
     const int t = quad * 32 + lane;                          // weight row of the tile
-    // Above 128 tokens a group's x slot is also that of the groups two stages
-    // away: its last stage before `it` must be done before an adapter
-    // stage writes the slot.  Waited for at every stage, so that no phase of
-    // that barrier is skipped.
+    const int ib = g % KB;                                   // the group's block within its stage
+    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    // prmt operand that completes a code byte to its table address
+    const uint32_t lut_base = kSgTableAt | (static_cast<uint32_t>(lane) * 8u);
+    // Above 64 tokens a group's x slot is also that of the groups two stages
+    // away: its last stage before `it` must be done before an adapter stage
+    // writes the slot.  Waited for at every stage, so that no phase of that
+    // barrier is skipped.
     auto x_done = [&](int it) { return it < 2 || wait_warp(aempty + (it - 2) % SA, ((it - 2) / SA) & 1u); };
-    for (int i = g; i < n_it * KB; i += kSgGroups) {         // 64-wide blocks of the stages
-      const int it = i / KB, s = it % S, sa = it % SA, ib = i % KB;
+    auto odd_term = [&](int m, int n) {
+      const int32_t a = tok_id[m];
+      return a < 0 ? 0.f : slots_odd_term(args.B + (static_cast<int64_t>(a) * args.out + n) * args.r,
+                                          args.us + static_cast<int64_t>(m) * args.r8, args.r);
+    };
+    uint32_t dph = 0;
+    auto dec_sync = [&]() {                                  // all dequant warps, bounded
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dec_bar);
+      const bool done = wait_warp(dec_bar, dph);
+      dph ^= 1u;
+      return done;
+    };
+    int uu = uu0, tile = tile0, seg = 0, cs = 0, seg_uu = uu0;
+    uint32_t cph = 0;
+    bool ok = true;
+    for (int i = 0; i < n_u && ok; ++i) {
+      const int it = i * SPU + g / KB, sa = it % SA;
       uint32_t v[32];
-      if (it < n_base) {
-        const int k = i >> 2, cs = k % kSgUnits, blk = i & 3;
-        const uint32_t par = (k / kSgUnits) & 1u;
-        if (!wait_warp(cfull + cs, par) || !wait_warp(sfull + cs, par)) break;
+      if (uu < UB) {
+        if (!(ok = wait_warp(cfull + cs, cph) && wait_warp(sfull + cs, cph))) break;
         const uint32_t crow = smem_u32(c_ring + cs * kSgCodeTile) + t * 128;
         uint32_t c[8];
-        lds_v4(crow + (((2 * blk) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[0]));
-        lds_v4(crow + (((2 * blk + 1) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[4]));
-        const float c_hat = s_ring[(cs * 4 + blk) * kSgRows + t];
+        lds_v4(crow + (((2 * g) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[0]));
+        lds_v4(crow + (((2 * g + 1) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[4]));
+        const float c_hat = s_ring[(cs * 4 + g) * kSgRows + t];
         __syncwarp();
         if (lane == 0) mbar_arrive(cempty + cs);
-        const Nf4Table tb = make_table(args.L, c_hat);
+        if (++cs == kSgUnits) { cs = 0; cph ^= 1u; }
+        if (kLut) {
+          uint64_t c2;
+          asm("mov.b64 %0, {%1, %1};" : "=l"(c2) : "f"(c_hat));
 #pragma unroll
-        for (int w = 0; w < 8; ++w) {
-          uint32_t o[4];
-          decode8(tb, c[w], o);
-          v[4 * w] = o[0]; v[4 * w + 1] = o[1]; v[4 * w + 2] = o[2]; v[4 * w + 3] = o[3];
+          for (int w = 0; w < 8; ++w) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              // bytes of the address: {lane copy, code byte, table, 0}
+              const uint32_t addr = prmt(lut_base, c[w], 0x3200u | ((4u + b) << 4));
+              uint64_t lv;
+              asm volatile("ld.shared.b64 %0, [%1];" : "=l"(lv) : "r"(addr));
+              asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(lv) : "l"(c2));
+              float lo, hi2;
+              asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi2) : "l"(lv));
+              v[4 * w + b] = pack_bf16x2_rn(lo, hi2);
+            }
+          }
+        } else {
+          const Nf4Table tb = make_table(args.L, c_hat);
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            uint32_t o[4];
+            decode8(tb, c[w], o);
+            v[4 * w] = o[0]; v[4 * w + 1] = o[1]; v[4 * w + 2] = o[2]; v[4 * w + 3] = o[3];
+          }
         }
-        if (!wait_warp(aempty + sa, ((it / SA) & 1u) ^ 1u)) break;
+        if (!(ok = wait_warp(aempty + sa, ((it / SA) & 1u) ^ 1u))) break;
       } else {
-        // adapter stage: rank columns [64 e, 64 e + 64) of the listed adapters, in chunks of 8
-        const int e = (l_begin + it - n_base) * KB + ib;
-        const bool row_ok = n0 + t < args.out;
-        if (!wait_warp(aempty + sa, ((it / SA) & 1u) ^ 1u)) break;
-        if (SA > S && !x_done(it)) break;
-        const uint32_t x_base = smem_u32(x_ring + s * x_stage + ib * x_blk);
+        // adapter block: rank columns [64 e, 64 e + 64) of the listed adapters, in chunks of 8
+        const int e = (uu - UB) * 4 + g;
+        const int row = tile * kSgRows + t;
+        const bool row_ok = row < args.out;
+        grid_dependency_wait();                              // us comes from the kernel before
+        if (!(ok = wait_warp(aempty + sa, ((it / SA) & 1u) ^ 1u))) break;
+        if (SA > S && !(ok = x_done(it))) break;
+        const uint32_t x_base = smem_u32(x_ring + (it % S) * x_stage + ib * x_blk);
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
           const int kk = e * 64 + ch * 8;
@@ -443,7 +562,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
           const int32_t a = live ? list[li] : -2;
           uint4 bv = make_uint4(0, 0, 0, 0);
           if (live && row_ok) {
-            const uint16_t* src = args.B + (static_cast<int64_t>(a) * args.out + n0 + t) * args.r + j0;
+            const uint16_t* src = args.B + (static_cast<int64_t>(a) * args.out + row) * args.r + j0;
             if ((args.r & 7) == 0) {
               bv = ld_nc_v4(src);
             } else {
@@ -456,91 +575,118 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
           v[4 * ch] = bv.x; v[4 * ch + 1] = bv.y; v[4 * ch + 2] = bv.z; v[4 * ch + 3] = bv.w;
 #pragma unroll
           for (int w = 4 * ch; w < 4 * ch + 4; ++w) {
-            if ((v[w] & 0x7F80u) == 0x7F80u) { v[w] &= 0xFFFF0000u; *odd = 1; }
-            if ((v[w] & 0x7F800000u) == 0x7F800000u) { v[w] &= 0xFFFFu; *odd = 1; }
+            if ((v[w] & 0x7F80u) == 0x7F80u) { v[w] &= 0xFFFF0000u; odd[seg & 1] = 1; }
+            if ((v[w] & 0x7F800000u) == 0x7F800000u) { v[w] &= 0xFFFFu; odd[seg & 1] = 1; }
           }
           for (int m = t; m < N; m += 128) {
             uint4 u = make_uint4(0, 0, 0, 0);
-            if (tok_id[m] == a) u = *reinterpret_cast<const uint4*>(args.us + static_cast<int64_t>(m0 + m) * args.r8 + j0);
+            if (tok_id[m] == a) u = *reinterpret_cast<const uint4*>(args.us + static_cast<int64_t>(m) * args.r8 + j0);
             sts_v4(x_base + m * 128 + ((ch ^ (m & 7)) << 4), u.x, u.y, u.z, u.w);
           }
         }
         fence_proxy_async_smem();                            // generic writes before the UMMA reads
       }
-      tmem_st_32x32b_x32(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + (sa * KB + ib) * 32, v);
+      tmem_st_32x32b_x32(a_lane + (sa * KB + ib) * 32, v);
       tmem_st_wait();
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(afull + sa);
-      if (SA > S && it < n_base && !x_done(it)) break;
+      if (SA > S && uu < UB && !(ok = x_done(it))) break;
+
+      if (++uu != UPT && i != n_u - 1) continue;
+      // ---------------------------------------------------------- the segment ends
+      const bool whole = seg_uu == 0 && uu == UPT;           // this CTA holds all of the tile
+      const int n0 = tile * kSgRows;
+      if (!(ok = wait_warp(acc_full, seg & 1u))) break;
+      tc_fence_after_sync();
+      const int my_odd = odd[seg & 1];
+      float* part = args.part + (static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0 ? 1 : 0)) * N * kSgRows;
+      for (int c0 = g * 16; c0 < N; c0 += 16 * kSgGroups) {
+        uint32_t d[16];
+        tmem_ld_32x32b_x16(a_lane + kSgAccCol + c0, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int m = c0 + k;
+          if (!whole) {
+            part[m * kSgRows + t] = __uint_as_float(d[k]);
+          } else if (m < args.M && n0 + t < args.out) {
+            float f = __uint_as_float(d[k]);
+            if (my_odd) f += odd_term(m, n0 + t);
+            args.h[static_cast<int64_t>(m) * args.out + n0 + t] = __bfloat16_as_ushort(__float2bfloat16_rn(f));
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      if (!whole) __threadfence();
+      if (!(ok = dec_sync())) break;
+      if (threadIdx.x == 256) odd[seg & 1] = 0;              // written again two segments on
+      if (!whole) {
+        // CTAs that hold units of this tile, in order: c_first .. c_last
+        const int64_t u_lo = static_cast<int64_t>(tile) * UPT, u_hi = u_lo + UPT;
+        int c_first = static_cast<int>(u_lo * G / T), c_last = static_cast<int>((u_hi - 1) * G / T);
+        while (c_first + 1 < G && sg_unit_begin(c_first + 1, T, G) <= u_lo) ++c_first;
+        while (c_first > 0 && sg_unit_begin(c_first, T, G) > u_lo) --c_first;
+        while (c_last + 1 < G && sg_unit_begin(c_last + 1, T, G) < u_hi) ++c_last;
+        while (c_last > 0 && sg_unit_begin(c_last, T, G) >= u_hi) --c_last;
+        const int n_parts = c_last - c_first + 1;
+        if (threadIdx.x == 256) {
+          grid_dependency_wait();                            // the kernel before zeroes the tickets
+          const uint32_t old = atomicAdd(args.tickets + tile, 1u | (my_odd ? 0x10000u : 0u));
+          last_flag[0] = (old & 0xFFFFu) == static_cast<uint32_t>(n_parts - 1);
+          last_flag[1] = (old >> 16) != 0 || my_odd;
+        }
+        // where each of them left its part: its first tile's, or its last one's
+        if (threadIdx.x - 256 < n_parts) {
+          const int c = c_first + static_cast<int>(threadIdx.x) - 256;
+          parts[threadIdx.x - 256] = 2 * c + (sg_unit_begin(c, T, G) / UPT == tile ? 0 : 1);
+        }
+        if (!(ok = dec_sync())) break;
+        if (last_flag[0]) {
+          __threadfence();
+          const bool any_odd = last_flag[1] != 0;
+          const int n = n0 + 4 * lane;
+          for (int m = warp - 8; m < args.M; m += kSgDecThreads / 32) {     // one warp per token, four rows per lane
+            float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p0 = 0; p0 < n_parts; p0 += 4) {        // four loads in flight, added in CTA order
+              float4 p[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                p[k] = p0 + k < n_parts
+                           ? __ldcg(reinterpret_cast<const float4*>(
+                                 args.part + (static_cast<int64_t>(parts[p0 + k]) * N + m) * kSgRows + 4 * lane))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) { d.x += p[k].x; d.y += p[k].y; d.z += p[k].z; d.w += p[k].w; }
+            }
+            if (n < args.out) {
+              if (any_odd) {
+                d.x += odd_term(m, n);
+                d.y += odd_term(m, n + 1);
+                d.z += odd_term(m, n + 2);
+                d.w += odd_term(m, n + 3);
+              }
+              *reinterpret_cast<uint2*>(args.h + static_cast<int64_t>(m) * args.out + n) =
+                  make_uint2(pack_bf16x2_rn(d.x, d.y), pack_bf16x2_rn(d.z, d.w));
+            }
+          }
+        }
+        if (!(ok = dec_sync())) break;                       // last_flag and parts are read
+      }
+      ++seg;
+      seg_uu = 0;
+      if (uu == UPT) { uu = 0; ++tile; }
     }
   }
 
-  // ---------------------------------------------------------------- epilogue
   __syncwarp();
-  wait(acc_full, 0);
-  tc_fence_after_sync();
-  __syncthreads();                                           // every copy has landed, every stage is read
-  float* part = reinterpret_cast<float*>(smem);              // [token][row], over the rings
-  if (warp >= 8) {
-    const int quad = warp & 3;
-    for (int c0 = ((warp - 8) >> 2) * 16; c0 < N; c0 += 16 * kSgGroups) {
-      uint32_t v[16];
-      tmem_ld_32x32b_x16(tmem_base + kSgAccCol + (static_cast<uint32_t>(quad * 32) << 16) + c0, v);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 16; ++i) part[(c0 + i) * kSgRows + quad * 32 + lane] = __uint_as_float(v[i]);
-    }
-  }
   tc_fence_before_sync();
   __syncthreads();
-  if (ks > 1) cluster_sync_all();                            // every CTA's partial is in place
-  int any_odd = 0;
-  for (int rk = 0; rk < ks; ++rk) {
-    int o;
-    if (ks == 1) o = *odd;
-    else asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(o) : "r"(mapa_shared(smem_u32(odd), rk)) : "memory");
-    any_odd |= o;
-  }
-  // this CTA's tokens: split, split + ks, ...; one warp per token, four rows per lane
-  const int n = n0 + 4 * lane;
-  for (int t = split + ks * warp; t < N; t += ks * (kSgThreads / 32)) {
-    const int m = m0 + t;
-    if (m >= args.M) break;
-    const uint32_t addr = smem_u32(part + t * kSgRows + 4 * lane);
-    float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int rk = 0; rk < ks; ++rk) {
-      float4 p;
-      if (ks == 1) {
-        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w)
-                     : "r"(addr) : "memory");
-      } else {
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w) : "r"(mapa_shared(addr, rk)) : "memory");
-      }
-      d.x += p.x; d.y += p.y; d.z += p.z; d.w += p.w;
-    }
-    if (any_odd && n < args.out && tok_id[t] >= 0) {         // the products left out of the stages
-      float* dd[4] = {&d.x, &d.y, &d.z, &d.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint16_t* src = args.B + (static_cast<int64_t>(tok_id[t]) * args.out + n + e) * args.r;
-        for (int j = 0; j < args.r; ++j) {
-          const uint32_t b = __ldg(src + j);
-          if ((b & 0x7F80u) == 0x7F80u)
-            *dd[e] = fmaf(__uint_as_float(static_cast<uint32_t>(args.us[static_cast<int64_t>(m) * args.r8 + j]) << 16),
-                          __uint_as_float(b << 16), *dd[e]);
-        }
-      }
-    }
-    if (n < args.out)
-      *reinterpret_cast<uint2*>(args.h + static_cast<int64_t>(m) * args.out + n) =
-          make_uint2(pack_bf16x2_rn(d.x, d.y), pack_bf16x2_rn(d.z, d.w));
-  }
-  if (ks > 1) cluster_sync_all();                            // no CTA leaves while others read it
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem_base, static_cast<uint32_t>(sg_tmem_cols(N)));
+    tmem_dealloc(tmem_base, kSgTmemCols);
   }
 }
 

@@ -90,32 +90,43 @@ __global__ void __launch_bounds__(kTsThreads) token_slots_kernel(const int32_t* 
   }
 }
 
-// One warp per (token, 8 rank columns): lane l takes the 8-column chunks
-// l, l + 32, ... of the token's row.  us has rows of r8 = r rounded up to 8;
-// its columns past r, and the rows of tokens without an adapter, are zero.
-__global__ void __launch_bounds__(256) slots_us_kernel(const uint16_t* __restrict__ x,
-                                                       const uint16_t* __restrict__ A,
-                                                       const float* __restrict__ scale,
-                                                       const int32_t* __restrict__ ids, int64_t M, int64_t K,
-                                                       int64_t n_adapters, int r, int r8, uint16_t* __restrict__ us) {
-  const int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const int64_t m = item / (r8 / 8);
-  const int j0 = static_cast<int>(item % (r8 / 8)) * 8;
-  if (m >= M) return;
+// us of a few tokens.  One CTA per (token, 4 rank columns): its warps share
+// the K axis (thread t takes the 8-column chunks t, t + 256, ...), then add up
+// over a butterfly and shared memory in warp order.  us has rows of r8 = r
+// rounded up to 8; its columns past r, and the rows of tokens without an
+// adapter, are zero.  Bound by the adapters' bytes, or by latency.  The CTAs
+// also zero the tickets of the GEMM behind, and let it start beside them.
+constexpr int kUsThreads = 256;
+constexpr int kUsRanks = 4;
+
+__global__ void __launch_bounds__(kUsThreads) slots_us_kernel(
+    const uint16_t* __restrict__ x, const uint16_t* __restrict__ A, const float* __restrict__ scale,
+    const int32_t* __restrict__ ids, int64_t K, int64_t n_adapters, int r, int r8, uint16_t* __restrict__ us,
+    uint32_t* __restrict__ tickets, int n_tickets) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float sums[kUsThreads / 32][kUsRanks];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = blockIdx.x * kUsThreads + threadIdx.x; i < n_tickets; i += gridDim.x * kUsThreads) tickets[i] = 0u;
+  const int per_tok = r8 / kUsRanks;
+  const int64_t m = blockIdx.x / per_tok;
+  const int j0 = static_cast<int>(blockIdx.x % per_tok) * kUsRanks;
   const int32_t a = __ldg(ids + m);
-  float acc[8] = {};
-  float s = 0.f;
-  if (a >= 0 && a < n_adapters) {
-    s = __ldg(scale + a);
-    for (int64_t c = lane; c < K / 8; c += 32) {
+  const bool has = a >= 0 && a < n_adapters;
+  float acc[kUsRanks] = {};
+  if (has) {
+    const uint16_t* Ar = A + (static_cast<int64_t>(a) * r + j0) * K;
+    const int chunks = static_cast<int>(K / 8);
+#pragma unroll 2
+    for (int c = threadIdx.x; c < chunks; c += kUsThreads) {
       const uint4 xv = ld_nc_v4(x + m * K + c * 8);
+      uint4 av[kUsRanks];
+#pragma unroll
+      for (int j = 0; j < kUsRanks; ++j)
+        av[j] = j0 + j < r ? ld_nc_v4(Ar + j * K + c * 8) : make_uint4(0, 0, 0, 0);
       const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j0 + j >= r) break;
-        const uint4 av = ld_nc_v4(A + (static_cast<int64_t>(a) * r + j0 + j) * K + c * 8);
-        const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
+      for (int j = 0; j < kUsRanks; ++j) {
+        const uint32_t aw[4] = {av[j].x, av[j].y, av[j].z, av[j].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           acc[j] = fmaf(fewtok_bf16_lo(xw[e]), fewtok_bf16_lo(aw[e]), acc[j]);
@@ -125,10 +136,19 @@ __global__ void __launch_bounds__(256) slots_us_kernel(const uint16_t* __restric
     }
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < kUsRanks; ++j) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], off);
-    if (lane == j) us[m * r8 + j0 + j] = __bfloat16_as_ushort(__float2bfloat16_rn(s * acc[j]));
+    if (lane == 0) sums[warp][j] = acc[j];
+  }
+  __syncthreads();
+  if (threadIdx.x < kUsRanks) {
+    float v = 0.f;
+    if (has && j0 + static_cast<int>(threadIdx.x) < r) {     // (a NaN in x times a zero of the padding is no result)
+      for (int w = 0; w < kUsThreads / 32; ++w) v += sums[w][threadIdx.x];
+      v *= __ldg(scale + a);
+    }
+    us[m * r8 + j0 + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
   }
 }
 
