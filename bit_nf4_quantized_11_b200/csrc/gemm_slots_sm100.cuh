@@ -75,7 +75,7 @@ __host__ __device__ constexpr bool sg_lut(int N) { return N <= 128; }
 // and barriers before it.  Without the table x starts at the boundary.
 constexpr uint32_t kSgTableAt = 0x10000;
 __host__ __device__ constexpr int sg_low_bytes() {
-  return kSgUnits * (kSgCodeTile + kSgRows * 16) + 2 * kSgMaxN * 4 + kSgMaxCtas * 4 + 64 + 512;
+  return kSgUnits * (kSgCodeTile + kSgRows * 16) + 3 * kSgMaxN * 4 + kSgMaxCtas * 4 + 64 + 512;
 }
 __host__ __device__ constexpr int sg_smem_bytes(int N) {   // (the window starts at or above address 0)
   return static_cast<int>(kSgTableAt) + (sg_lut(N) ? 65536 + sg_stages(N) * sg_kb(N) * N * 128 : 131072);
@@ -209,10 +209,11 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   float* s_ring = reinterpret_cast<float*>(c_ring + kSgUnits * kSgCodeTile);   // [unit][block][row]
   int32_t* tok_id = reinterpret_cast<int32_t*>(s_ring + kSgUnits * kSgRows * 4);
   int32_t* list = tok_id + kSgMaxN;                          // distinct adapters, first appearance first
-  int32_t* parts = list + kSgMaxN;                           // the partials of the tile being added up
+  int32_t* tok_col = list + kSgMaxN;                         // a token's first rank column, or far past the last
+  int32_t* parts = tok_col + kSgMaxN;                        // the partials of the tile being added up
   int32_t* counts = parts + kSgMaxCtas;                      // [8] leaders per warp of 32 tokens
   volatile int32_t* odd = counts + 8;                        // [2] by segment: a B value was not finite
-  volatile int32_t* last_flag = counts + 10;                 // [2] this CTA adds the tile up; some part was odd
+  volatile int32_t* last_flag = counts + 10;                 // [2 segments][2]: this CTA adds the tile up; some part was odd
   uint8_t* x_ring = kLut ? table + 65536 : table;
   uint64_t* bars = reinterpret_cast<uint64_t*>(counts + 16);
   uint64_t* xfull = bars;                                    // the stage's x tile landed
@@ -220,7 +221,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   uint64_t* afull = xempty + kSgMaxStages;                   // the stage's A operand is written
   uint64_t* aempty = afull + kSgMaxStages;                   // the UMMAs on it finished
   uint64_t* cfull = aempty + kSgMaxStages;                   // the code tile landed
-  uint64_t* sfull = cfull + kSgUnits;                        // its scales are written
+  uint64_t* sfull = cfull + kSgUnits;                        // its scales are written too
   uint64_t* cempty = sfull + kSgUnits;                       // codes and scales are read
   uint64_t* acc_full = cempty + kSgUnits;                    // a segment's accumulator is complete
   uint64_t* acc_empty = acc_full + 1;                        // and read
@@ -274,16 +275,8 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   }
   if (kLut) {
     // row b (256 bytes): lane l's copy of {level of the low code, level of the high code} at 8 l
-    for (int e = threadIdx.x; e < 256 * 16; e += kSgThreads) {
-      const int b = e >> 4;
-      float lo = 0.f, hi = 0.f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if ((b & 15) == j) lo = args.L.v[j];
-        if ((b >> 4) == j) hi = args.L.v[j];
-      }
-      *reinterpret_cast<float4*>(table + e * 16) = make_float4(lo, hi, lo, hi);
-    }
+    for (int b = warp; b < 256; b += kSgThreads / 32)
+      *reinterpret_cast<float2*>(table + b * 256 + lane * 8) = make_float2(args.L.v[b & 15], args.L.v[b >> 4]);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -309,6 +302,19 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
     }
     const uint32_t b = __ballot_sync(0xFFFFFFFFu, leader);
     if (leader) list[before + __popc(b & ((1u << lane) - 1u))] = my_id;
+  }
+  __syncthreads();
+  if (threadIdx.x < kSgMaxN) {                               // read by the dequant groups behind the next barrier
+    int li = -1;
+    const int4* l4 = reinterpret_cast<const int4*>(list);
+    for (int i = 0; my_id >= 0 && 4 * i < n_list && li < 0; ++i) {
+      const int4 o = l4[i];                                  // (entries past the list are not looked at first)
+      if (o.x == my_id) li = 4 * i;
+      else if (o.y == my_id && 4 * i + 1 < n_list) li = 4 * i + 1;
+      else if (o.z == my_id && 4 * i + 2 < n_list) li = 4 * i + 2;
+      else if (o.w == my_id && 4 * i + 3 < n_list) li = 4 * i + 3;
+    }
+    tok_col[threadIdx.x] = li < 0 ? -(1 << 29) : li * args.r8;
   }
   __syncthreads();
   const uint32_t tmem_base = *tmem_holder;
@@ -469,6 +475,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
           const int q = static_cast<int8_t>(cur.q >> (8 * e));
           s_ring[(s * 4 + e) * kSgRows + t] = row < args.out && 4 * uu + e < n_blk ? block_scale(q, st, mu) : 0.f;
         }
+        if (!wait_warp(cfull + s, ph ^ 1u)) break;           // codes too: the dequant groups wait for sfull alone
         __syncwarp();
         if (lane == 0) mbar_arrive(sfull + s);
         if (++s == kSgUnits) { s = 0; ph ^= 1u; }
@@ -502,14 +509,26 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       dph ^= 1u;
       return done;
     };
+    // The tensor-memory store of a block completes while the next one is being
+    // read: its arrive waits until then.
+    int stored = -1;                                         // A stage with a store under way
+    auto flush = [&]() {
+      if (stored < 0) return;
+      tmem_st_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(afull + stored);
+      stored = -1;
+    };
     int uu = uu0, tile = tile0, seg = 0, cs = 0, seg_uu = uu0;
     uint32_t cph = 0;
+    int cut_first = -1, cut_last = -1;                       // this CTA's cut tiles
     bool ok = true;
     for (int i = 0; i < n_u && ok; ++i) {
       const int it = i * SPU + g / KB, sa = it % SA;
       uint32_t v[32];
       if (uu < UB) {
-        if (!(ok = wait_warp(cfull + cs, cph) && wait_warp(sfull + cs, cph))) break;
+        if (!(ok = wait_warp(sfull + cs, cph))) break;
         const uint32_t crow = smem_u32(c_ring + cs * kSgCodeTile) + t * 128;
         uint32_t c[8];
         lds_v4(crow + (((2 * g) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[0]));
@@ -518,6 +537,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(cempty + cs);
         if (++cs == kSgUnits) { cs = 0; cph ^= 1u; }
+        flush();
         if (kLut) {
           uint64_t c2;
           asm("mov.b64 %0, {%1, %1};" : "=l"(c2) : "f"(c_hat));
@@ -550,19 +570,14 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
         const int e = (uu - UB) * 4 + g;
         const int row = tile * kSgRows + t;
         const bool row_ok = row < args.out;
-        grid_dependency_wait();                              // us comes from the kernel before
-        if (!(ok = wait_warp(aempty + sa, ((it / SA) & 1u) ^ 1u))) break;
-        if (SA > S && !(ok = x_done(it))) break;
-        const uint32_t x_base = smem_u32(x_ring + (it % S) * x_stage + ib * x_blk);
+        flush();
+        // the 8 chunks of this row's B values, all loads under way together
+        int li = e * 64 / args.r8, j0 = e * 64 - li * args.r8;
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
-          const int kk = e * 64 + ch * 8;
-          const int li = kk / args.r8, j0 = kk - li * args.r8;
-          const bool live = kk < k_low;
-          const int32_t a = live ? list[li] : -2;
           uint4 bv = make_uint4(0, 0, 0, 0);
-          if (live && row_ok) {
-            const uint16_t* src = args.B + (static_cast<int64_t>(a) * args.out + row) * args.r + j0;
+          if (row_ok && li < n_list) {
+            const uint16_t* src = args.B + (static_cast<int64_t>(list[li]) * args.out + row) * args.r + j0;
             if ((args.r & 7) == 0) {
               bv = ld_nc_v4(src);
             } else {
@@ -573,30 +588,48 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
             }
           }
           v[4 * ch] = bv.x; v[4 * ch + 1] = bv.y; v[4 * ch + 2] = bv.z; v[4 * ch + 3] = bv.w;
+          j0 += 8;
+          if (j0 == args.r8) { j0 = 0; ++li; }
+        }
+        if (!(ok = wait_warp(aempty + sa, ((it / SA) & 1u) ^ 1u))) break;
+        if (SA > S && !(ok = x_done(it))) break;
+        grid_dependency_wait();                              // us comes from the kernel before
+        // the tokens' us under the columns of their own adapter, zero elsewhere
+        const uint32_t x_base = smem_u32(x_ring + (it % S) * x_stage + ib * x_blk);
+        for (int m = t; m < N; m += 128) {
+          const uint32_t x_row = x_base + m * 128;
 #pragma unroll
-          for (int w = 4 * ch; w < 4 * ch + 4; ++w) {
-            if ((v[w] & 0x7F80u) == 0x7F80u) { v[w] &= 0xFFFF0000u; odd[seg & 1] = 1; }
-            if ((v[w] & 0x7F800000u) == 0x7F800000u) { v[w] &= 0xFFFFu; odd[seg & 1] = 1; }
-          }
-          for (int m = t; m < N; m += 128) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (tok_id[m] == a) u = *reinterpret_cast<const uint4*>(args.us + static_cast<int64_t>(m) * args.r8 + j0);
-            sts_v4(x_base + m * 128 + ((ch ^ (m & 7)) << 4), u.x, u.y, u.z, u.w);
+          for (int ch = 0; ch < 8; ++ch) sts_v4(x_row + (ch << 4), 0, 0, 0, 0);
+          const int col = tok_col[m] - e * 64;               // the token's first column in this block
+          const uint16_t* src = args.us + static_cast<int64_t>(m) * args.r8;
+#pragma unroll 2
+          for (int j = max(0, -col); j < args.r8 && col + j < 64; j += 8) {
+            const uint4 u = *reinterpret_cast<const uint4*>(src + j);
+            sts_v4(x_row + ((((col + j) >> 3) ^ (m & 7)) << 4), u.x, u.y, u.z, u.w);
           }
         }
         fence_proxy_async_smem();                            // generic writes before the UMMA reads
+        uint32_t exps = 0;                                   // bit 15 or 31: an exponent of all ones
+#pragma unroll
+        for (int w = 0; w < 32; ++w) exps |= (v[w] & 0x7F807F80u) + 0x00800080u;
+        if (exps & 0x80008000u) {
+          odd[seg & 1] = 1;
+#pragma unroll
+          for (int w = 0; w < 32; ++w) {
+            if ((v[w] & 0x7F80u) == 0x7F80u) v[w] &= 0xFFFF0000u;
+            if ((v[w] & 0x7F800000u) == 0x7F800000u) v[w] &= 0xFFFFu;
+          }
+        }
       }
       tmem_st_32x32b_x32(a_lane + (sa * KB + ib) * 32, v);
-      tmem_st_wait();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(afull + sa);
+      stored = sa;
       if (SA > S && uu < UB && !(ok = x_done(it))) break;
 
       if (++uu != UPT && i != n_u - 1) continue;
       // ---------------------------------------------------------- the segment ends
       const bool whole = seg_uu == 0 && uu == UPT;           // this CTA holds all of the tile
       const int n0 = tile * kSgRows;
+      flush();
       if (!(ok = wait_warp(acc_full, seg & 1u))) break;
       tc_fence_after_sync();
       const int my_odd = odd[seg & 1];
@@ -624,60 +657,71 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       if (!(ok = dec_sync())) break;
       if (threadIdx.x == 256) odd[seg & 1] = 0;              // written again two segments on
       if (!whole) {
-        // CTAs that hold units of this tile, in order: c_first .. c_last
-        const int64_t u_lo = static_cast<int64_t>(tile) * UPT, u_hi = u_lo + UPT;
-        int c_first = static_cast<int>(u_lo * G / T), c_last = static_cast<int>((u_hi - 1) * G / T);
-        while (c_first + 1 < G && sg_unit_begin(c_first + 1, T, G) <= u_lo) ++c_first;
-        while (c_first > 0 && sg_unit_begin(c_first, T, G) > u_lo) --c_first;
-        while (c_last + 1 < G && sg_unit_begin(c_last + 1, T, G) < u_hi) ++c_last;
-        while (c_last > 0 && sg_unit_begin(c_last, T, G) >= u_hi) --c_last;
-        const int n_parts = c_last - c_first + 1;
+        // the answer is read when this CTA is done with its units: the part
+        // that ends here is rarely the tile's last
+        const int c = seg > 0 ? 1 : 0;
+        if (seg > 0) cut_last = tile;
+        else cut_first = tile;
         if (threadIdx.x == 256) {
           grid_dependency_wait();                            // the kernel before zeroes the tickets
-          const uint32_t old = atomicAdd(args.tickets + tile, 1u | (my_odd ? 0x10000u : 0u));
-          last_flag[0] = (old & 0xFFFFu) == static_cast<uint32_t>(n_parts - 1);
-          last_flag[1] = (old >> 16) != 0 || my_odd;
+          last_flag[2 * c] = static_cast<int32_t>(atomicAdd(args.tickets + tile, 1u | (my_odd ? 0x10000u : 0u)));
+          last_flag[2 * c + 1] = my_odd;
         }
-        // where each of them left its part: its first tile's, or its last one's
-        if (threadIdx.x - 256 < n_parts) {
-          const int c = c_first + static_cast<int>(threadIdx.x) - 256;
-          parts[threadIdx.x - 256] = 2 * c + (sg_unit_begin(c, T, G) / UPT == tile ? 0 : 1);
-        }
-        if (!(ok = dec_sync())) break;
-        if (last_flag[0]) {
-          __threadfence();
-          const bool any_odd = last_flag[1] != 0;
-          const int n = n0 + 4 * lane;
-          for (int m = warp - 8; m < args.M; m += kSgDecThreads / 32) {     // one warp per token, four rows per lane
-            float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p0 = 0; p0 < n_parts; p0 += 4) {        // four loads in flight, added in CTA order
-              float4 p[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                p[k] = p0 + k < n_parts
-                           ? __ldcg(reinterpret_cast<const float4*>(
-                                 args.part + (static_cast<int64_t>(parts[p0 + k]) * N + m) * kSgRows + 4 * lane))
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) { d.x += p[k].x; d.y += p[k].y; d.z += p[k].z; d.w += p[k].w; }
-            }
-            if (n < args.out) {
-              if (any_odd) {
-                d.x += odd_term(m, n);
-                d.y += odd_term(m, n + 1);
-                d.z += odd_term(m, n + 2);
-                d.w += odd_term(m, n + 3);
-              }
-              *reinterpret_cast<uint2*>(args.h + static_cast<int64_t>(m) * args.out + n) =
-                  make_uint2(pack_bf16x2_rn(d.x, d.y), pack_bf16x2_rn(d.z, d.w));
-            }
-          }
-        }
-        if (!(ok = dec_sync())) break;                       // last_flag and parts are read
       }
       ++seg;
       seg_uu = 0;
       if (uu == UPT) { uu = 0; ++tile; }
+    }
+    // ------------------------------------------------------------ tiles cut between CTAs
+#pragma unroll 1
+    for (int c = 0; c < 2 && ok; ++c) {
+      const int tl = c == 0 ? cut_first : cut_last;
+      if (tl < 0) continue;
+      // CTAs that hold units of this tile, in order: c_first .. c_last
+      const int64_t u_lo = static_cast<int64_t>(tl) * UPT, u_hi = u_lo + UPT;
+      int c_first = static_cast<int>(u_lo * G / T), c_last = static_cast<int>((u_hi - 1) * G / T);
+      while (c_first + 1 < G && sg_unit_begin(c_first + 1, T, G) <= u_lo) ++c_first;
+      while (c_first > 0 && sg_unit_begin(c_first, T, G) > u_lo) --c_first;
+      while (c_last + 1 < G && sg_unit_begin(c_last + 1, T, G) < u_hi) ++c_last;
+      while (c_last > 0 && sg_unit_begin(c_last, T, G) >= u_hi) --c_last;
+      const int n_parts = c_last - c_first + 1;
+      // where each of them left its part: its first tile's, or its last one's
+      if (static_cast<int>(threadIdx.x) - 256 < n_parts) {
+        const int k = c_first + static_cast<int>(threadIdx.x) - 256;
+        parts[threadIdx.x - 256] = 2 * k + (sg_unit_begin(k, T, G) / UPT == tl ? 0 : 1);
+      }
+      if (!(ok = dec_sync())) break;
+      const uint32_t old = static_cast<uint32_t>(last_flag[2 * c]);
+      if ((old & 0xFFFFu) == static_cast<uint32_t>(n_parts - 1)) {
+        __threadfence();
+        const bool any_odd = (old >> 16) != 0 || last_flag[2 * c + 1] != 0;
+        const int n = tl * kSgRows + 4 * lane;
+        for (int m = warp - 8; m < args.M; m += kSgDecThreads / 32) {       // one warp per token, four rows per lane
+          float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int p0 = 0; p0 < n_parts; p0 += 4) {          // four loads in flight, added in CTA order
+            float4 p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              p[k] = p0 + k < n_parts
+                         ? __ldcg(reinterpret_cast<const float4*>(
+                               args.part + (static_cast<int64_t>(parts[p0 + k]) * N + m) * kSgRows + 4 * lane))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) { d.x += p[k].x; d.y += p[k].y; d.z += p[k].z; d.w += p[k].w; }
+          }
+          if (n < args.out) {
+            if (any_odd) {
+              d.x += odd_term(m, n);
+              d.y += odd_term(m, n + 1);
+              d.z += odd_term(m, n + 2);
+              d.w += odd_term(m, n + 3);
+            }
+            *reinterpret_cast<uint2*>(args.h + static_cast<int64_t>(m) * args.out + n) =
+                make_uint2(pack_bf16x2_rn(d.x, d.y), pack_bf16x2_rn(d.z, d.w));
+          }
+        }
+      }
+      if (!(ok = dec_sync())) break;                         // parts are read
     }
   }
 
