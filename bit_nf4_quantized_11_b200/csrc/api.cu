@@ -1018,6 +1018,12 @@ int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* 
     cfg.blockDim = dim3(qnf4::kSgThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
+    // may start while the rank-r kernel runs; it waits for it before it reads us or the tickets
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g_timing_on.load() ? 0 : 1;               // (timed launches one after another)
     {
       LaunchTimer lt_("slots_gemm", st);
       QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, tm_codes, tm_x, a));

@@ -56,6 +56,7 @@ namespace qnf4 {
 constexpr int kSgRows = 128;                  // weight rows per tile
 constexpr int kSgMaxN = 256;                  // tokens per launch
 constexpr int kSgMaxCtas = 256;
+constexpr int kSgHash = 512;
 constexpr int kSgUnits = 3;                   // code tiles in flight
 constexpr int kSgCodeTile = kSgRows * 128;    // 16 KB: 256 K columns
 constexpr int kSgABlocks = 8;                 // blocks of the tensor-memory A ring, 32 columns each
@@ -75,7 +76,7 @@ __host__ __device__ constexpr bool sg_lut(int N) { return N <= 128; }
 // and barriers before it.  Without the table x starts at the boundary.
 constexpr uint32_t kSgTableAt = 0x10000;
 __host__ __device__ constexpr int sg_low_bytes() {
-  return kSgUnits * (kSgCodeTile + kSgRows * 16) + 3 * kSgMaxN * 4 + kSgMaxCtas * 4 + 64 + 512;
+  return kSgUnits * (kSgCodeTile + kSgRows * 16) + 2 * kSgMaxN * 4 + kSgMaxCtas * 4 + 64 + 512;
 }
 __host__ __device__ constexpr int sg_smem_bytes(int N) {   // (the window starts at or above address 0)
   return static_cast<int>(kSgTableAt) + (sg_lut(N) ? 65536 + sg_stages(N) * sg_kb(N) * N * 128 : 131072);
@@ -207,8 +208,8 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   const int x_blk = N * 128, x_stage = KB * x_blk;
   uint8_t* c_ring = low;
   float* s_ring = reinterpret_cast<float*>(c_ring + kSgUnits * kSgCodeTile);   // [unit][block][row]
-  int32_t* tok_id = reinterpret_cast<int32_t*>(s_ring + kSgUnits * kSgRows * 4);
-  int32_t* list = tok_id + kSgMaxN;                          // distinct adapters, first appearance first
+  int32_t* list = reinterpret_cast<int32_t*>(s_ring + kSgUnits * kSgRows * 4);
+                                                                                    // distinct adapters, first appearance first
   int32_t* tok_col = list + kSgMaxN;                         // a token's first rank column, or far past the last
   int32_t* parts = tok_col + kSgMaxN;                        // the partials of the tile being added up
   int32_t* counts = parts + kSgMaxCtas;                      // [8] leaders per warp of 32 tokens
@@ -259,19 +260,19 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
     tmem_alloc(tmem_holder, kSgTmemCols);
     tmem_relinquish();
   }
-  // The tokens' slots, -1 for no adapter and for rows past the batch, and the
-  // distinct ones: a token leads if no token before it has its slot.
-  bool leader = false;
+  // The tokens' slots (-1: no adapter, or past the batch), and the distinct
+  // ones in order of first appearance: a hash table over the code ring, which
+  // is not in use yet, keeps each slot's first token.
+  int32_t* h_key = reinterpret_cast<int32_t*>(c_ring);
+  int32_t* h_first = h_key + kSgHash;
+  for (int i = threadIdx.x; i < kSgHash; i += kSgThreads) {
+    h_key[i] = -1;
+    h_first[i] = kSgMaxN;
+  }
   int32_t my_id = -1;
-  if (threadIdx.x < kSgMaxN) {                               // whole warps
-    const int t = threadIdx.x;
-    if (t < args.M) {
-      my_id = __ldg(args.ids + t);
-      if (my_id < 0 || my_id >= args.n_adapters) my_id = -1;
-    }
-    tok_id[t] = my_id;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, my_id);
-    leader = my_id >= 0 && (same & ((1u << lane) - 1u)) == 0;
+  if (threadIdx.x < kSgMaxN && static_cast<int>(threadIdx.x) < args.M) {
+    my_id = __ldg(args.ids + threadIdx.x);
+    if (my_id < 0 || my_id >= args.n_adapters) my_id = -1;
   }
   if (kLut) {
     // row b (256 bytes): lane l's copy of {level of the low code, level of the high code} at 8 l
@@ -281,41 +282,36 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (threadIdx.x < kSgMaxN) {
-    const int4* ids4 = reinterpret_cast<const int4*>(tok_id);
-    for (int i = 0; leader && i < warp * 8; ++i) {           // the warps before this one
-      const int4 o = ids4[i];
-      if (o.x == my_id || o.y == my_id || o.z == my_id || o.w == my_id) leader = false;
+  int slot = -1;                                             // the token's place in the hash table
+  if (my_id >= 0) {
+    slot = static_cast<int>((static_cast<uint32_t>(my_id) * 2654435761u) >> 23);   // 9 bits
+    while (true) {
+      const int32_t was = atomicCAS(h_key + slot, -1, my_id);
+      if (was == -1 || was == my_id) break;
+      slot = (slot + 1) & (kSgHash - 1);                     // at most 256 of 512 places are taken
     }
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, leader);
-    if (lane == 0) counts[warp] = __popc(b);
+    atomicMin(h_first + slot, static_cast<int32_t>(threadIdx.x));
   }
   __syncthreads();
-  int n_list = 0;
-  {
-    int before = 0;
+  const bool leader = slot >= 0 && h_first[slot] == static_cast<int32_t>(threadIdx.x);
+  const uint32_t lead = __ballot_sync(0xFFFFFFFFu, leader);
+  if (warp < kSgMaxN / 32 && lane == 0) counts[warp] = __popc(lead);
+  __syncthreads();
+  int n_list = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < kSgMaxN / 32; ++w) {
-      const int c = counts[w];
-      if (w < warp) before += c;
-      n_list += c;
-    }
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, leader);
-    if (leader) list[before + __popc(b & ((1u << lane) - 1u))] = my_id;
+  for (int w = 0; w < kSgMaxN / 32; ++w) {
+    const int c = counts[w];
+    if (w < warp) before += c;
+    n_list += c;
+  }
+  if (leader) {
+    const int li = before + __popc(lead & ((1u << lane) - 1u));
+    list[li] = my_id;
+    h_key[slot] = li;                                        // (the keys are not needed any more)
   }
   __syncthreads();
-  if (threadIdx.x < kSgMaxN) {                               // read by the dequant groups behind the next barrier
-    int li = -1;
-    const int4* l4 = reinterpret_cast<const int4*>(list);
-    for (int i = 0; my_id >= 0 && 4 * i < n_list && li < 0; ++i) {
-      const int4 o = l4[i];                                  // (entries past the list are not looked at first)
-      if (o.x == my_id) li = 4 * i;
-      else if (o.y == my_id && 4 * i + 1 < n_list) li = 4 * i + 1;
-      else if (o.z == my_id && 4 * i + 2 < n_list) li = 4 * i + 2;
-      else if (o.w == my_id && 4 * i + 3 < n_list) li = 4 * i + 3;
-    }
-    tok_col[threadIdx.x] = li < 0 ? -(1 << 29) : li * args.r8;
-  }
+  if (threadIdx.x < kSgMaxN) tok_col[threadIdx.x] = slot < 0 ? -(1 << 29) : h_key[slot] * args.r8;
+  fence_proxy_async_smem();                                  // the table's words before the copies over them
   __syncthreads();
   const uint32_t tmem_base = *tmem_holder;
   const int k_low = n_list * args.r8;                        // rank columns of the listed adapters
@@ -497,8 +493,9 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
     // barrier is skipped.
     auto x_done = [&](int it) { return it < 2 || wait_warp(aempty + (it - 2) % SA, ((it - 2) / SA) & 1u); };
     auto odd_term = [&](int m, int n) {
-      const int32_t a = tok_id[m];
-      return a < 0 ? 0.f : slots_odd_term(args.B + (static_cast<int64_t>(a) * args.out + n) * args.r,
+      if (tok_col[m] < 0) return 0.f;
+      const int64_t a = list[tok_col[m] / args.r8];
+      return slots_odd_term(args.B + (a * args.out + n) * args.r,
                                           args.us + static_cast<int64_t>(m) * args.r8, args.r);
     };
     uint32_t dph = 0;
@@ -599,7 +596,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
         for (int m = t; m < N; m += 128) {
           const uint32_t x_row = x_base + m * 128;
 #pragma unroll
-          for (int ch = 0; ch < 8; ++ch) sts_v4(x_row + (ch << 4), 0, 0, 0, 0);
+          for (int ch = 0; ch < 8; ++ch) sts_v4(x_row + ((ch ^ (m & 7)) << 4), 0, 0, 0, 0);
           const int col = tok_col[m] - e * 64;               // the token's first column in this block
           const uint16_t* src = args.us + static_cast<int64_t>(m) * args.r8;
 #pragma unroll 2
@@ -696,28 +693,43 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
         __threadfence();
         const bool any_odd = (old >> 16) != 0 || last_flag[2 * c + 1] != 0;
         const int n = tl * kSgRows + 4 * lane;
-        for (int m = warp - 8; m < args.M; m += kSgDecThreads / 32) {       // one warp per token, four rows per lane
-          float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p0 = 0; p0 < n_parts; p0 += 4) {          // four loads in flight, added in CTA order
-            float4 p[4];
+        // one warp per four tokens, four rows per lane; the parts of two CTAs
+        // are under way together, added in CTA order
+        for (int m0 = (warp - 8) * 4; m0 < args.M; m0 += kSgDecThreads / 32 * 4) {
+          float4 d[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              p[k] = p0 + k < n_parts
-                         ? __ldcg(reinterpret_cast<const float4*>(
-                               args.part + (static_cast<int64_t>(parts[p0 + k]) * N + m) * kSgRows + 4 * lane))
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < 4; ++k) d[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int p0 = 0; p0 < n_parts; p0 += 2) {
+            float4 p[2][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) { d.x += p[k].x; d.y += p[k].y; d.z += p[k].z; d.w += p[k].w; }
+            for (int j = 0; j < 2; ++j) {
+              const float* src = args.part + (static_cast<int64_t>(parts[min(p0 + j, n_parts - 1)]) * N + m0) * kSgRows +
+                                 4 * lane;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)                    // (rows up to N, a multiple of 16, are there)
+                p[j][k] = __ldcg(reinterpret_cast<const float4*>(src + k * kSgRows));
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (p0 + j >= n_parts) break;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                d[k].x += p[j][k].x; d[k].y += p[j][k].y; d[k].z += p[j][k].z; d[k].w += p[j][k].w;
+              }
+            }
           }
-          if (n < args.out) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int m = m0 + k;
+            if (m >= args.M || n >= args.out) break;
             if (any_odd) {
-              d.x += odd_term(m, n);
-              d.y += odd_term(m, n + 1);
-              d.z += odd_term(m, n + 2);
-              d.w += odd_term(m, n + 3);
+              d[k].x += odd_term(m, n);
+              d[k].y += odd_term(m, n + 1);
+              d[k].z += odd_term(m, n + 2);
+              d[k].w += odd_term(m, n + 3);
             }
             *reinterpret_cast<uint2*>(args.h + static_cast<int64_t>(m) * args.out + n) =
-                make_uint2(pack_bf16x2_rn(d.x, d.y), pack_bf16x2_rn(d.z, d.w));
+                make_uint2(pack_bf16x2_rn(d[k].x, d[k].y), pack_bf16x2_rn(d[k].z, d[k].w));
           }
         }
       }
