@@ -23,6 +23,7 @@ Entry points (same names as the C ABI, without the ``qlora_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -155,12 +156,25 @@ def _need(t, dtype, name, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _one_device(*tensors):
-    """All tensors live on the current device, whose stream the call uses."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+def _ready(dev: int, *specs):
+    """Checks of the calls that a server makes once per projection and step:
+    (tensor, dtype, name, shape) each, like :func:`_need`, and all tensors on
+    the current device `dev`, whose stream the call uses."""
+    for t, dtype, name, shape in specs:
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape
+                and t.is_contiguous()):
+            _need(t, dtype, name, shape)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current device cuda:{dev}, got {t.device}")
+
+
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+@functools.lru_cache(maxsize=1024)
+def _cached_workspace_size(op: int, M: int, in_features: int, out_features: int, r: int, dev: int) -> int:
+    return workspace_size(op, M, in_features, out_features, r)
 
 
 @dataclass
@@ -536,15 +550,13 @@ def token_slots(lengths, slots, n_tokens: int, out=None) -> torch.Tensor:
     """int32 [n_tokens]: the adapter slot of every token of requests that lie
     one after another (lengths and slots int32 [n_requests]); -1 for the
     tokens behind the last request."""
-    _need(lengths, torch.int32, "lengths")
-    _need(slots, torch.int32, "slots", lengths.shape)
-    if lengths.dim() != 1:
-        raise ValueError("lengths must have one dimension")
-    ids = out if out is not None else torch.empty(n_tokens, dtype=torch.int32, device=lengths.device)
-    _need(ids, torch.int32, "out", (n_tokens,))
-    _one_device(lengths, slots, ids)
-    _check(load().qlora_token_slots(_ptr(lengths), _ptr(slots), lengths.shape[0], int(n_tokens), _ptr(ids),
-                                    _stream()), "qlora_token_slots")
+    dev = torch.cuda.current_device()
+    n = lengths.shape[0] if isinstance(lengths, torch.Tensor) and lengths.dim() == 1 else -1
+    ids = out if out is not None else torch.empty(n_tokens, dtype=torch.int32, device=dev)
+    _ready(dev, (lengths, torch.int32, "lengths", (n,)), (slots, torch.int32, "slots", (n,)),
+           (ids, torch.int32, "out", (n_tokens,)))
+    _check(load().qlora_token_slots(lengths.data_ptr(), slots.data_ptr(), n, n_tokens, ids.data_ptr(),
+                                    _raw_stream(dev)), "qlora_token_slots")
     return ids
 
 
@@ -553,21 +565,21 @@ def linear_fwd_slots(x, w: NF4Weight, A, B, scale, ids, h=None, workspace=None):
     a = ids[m] (see :func:`token_slots`); a token with a slot outside [0, n)
     gets the base product alone.  A bf16 [n, r, in], B bf16 [n, out, r],
     scale fp32 [n], ids int32 [M]; returns h bf16 [M, out]."""
-    M = x.shape[0]
-    n, r = A.shape[0], A.shape[1]
-    _need(x, torch.bfloat16, "x", (M, w.cols))
-    _need(A, torch.bfloat16, "A", (n, r, w.cols))
-    _need(B, torch.bfloat16, "B", (n, w.rows, r))
-    _need(scale, torch.float32, "scale", (n,))
-    _need(ids, torch.int32, "ids", (M,))
-    h = h if h is not None else torch.empty((M, w.rows), dtype=torch.bfloat16, device=x.device)
-    _need(h, torch.bfloat16, "h", (M, w.rows))
-    _one_device(x, w.codes, A, B, scale, ids, h)
-    ws = _workspace(workspace_size(OP_LINEAR_FWD_SLOTS, M, w.cols, w.rows, r), x.device, workspace)
+    dev = torch.cuda.current_device()
+    M, (n, r, _) = x.shape[0], A.shape
+    rows, cols = w.rows, w.cols
+    h = h if h is not None else torch.empty((M, rows), dtype=torch.bfloat16, device=dev)
+    _ready(dev, (x, torch.bfloat16, "x", (M, cols)), (A, torch.bfloat16, "A", (n, r, cols)),
+           (B, torch.bfloat16, "B", (n, rows, r)), (scale, torch.float32, "scale", (n,)),
+           (ids, torch.int32, "ids", (M,)), (h, torch.bfloat16, "h", (M, rows)),
+           (w.codes, torch.uint8, "w.codes", (rows, cols // 2)))
+    ws = _workspace(_cached_workspace_size(OP_LINEAR_FWD_SLOTS, M, cols, rows, r, dev), x.device, workspace)
     cw = w._c()
-    _check(load().qlora_linear_fwd_slots(_ptr(x), M, ctypes.byref(cw), _ptr(A), _ptr(B), n, r, _ptr(scale), _ptr(ids),
-                                         _ptr(h), _ptr(ws), ws.numel() if ws is not None else 0, _stream()),
-           "qlora_linear_fwd_slots")
+    _check(load().qlora_linear_fwd_slots(x.data_ptr(), M, ctypes.byref(cw), A.data_ptr(), B.data_ptr(), n, r,
+                                         scale.data_ptr(), ids.data_ptr(), h.data_ptr(),
+                                         ws.data_ptr() if ws is not None else None,
+                                         ws.numel() if ws is not None else 0,
+                                         _raw_stream(dev)), "qlora_linear_fwd_slots")
     return h
 
 

@@ -27,6 +27,7 @@
 #include "fewtok.cuh"
 #include "slots.cuh"
 #include "gemm_slots_sm100.cuh"
+#include "slots_us_sm100.cuh"
 
 namespace qnf4_host {
 void build_codebook(float levels[16], float thresholds[15]);
@@ -519,20 +520,14 @@ int launch_gemm_pair(const qnf4::GemmArgs& args, const CUtensorMap& tm_act, cons
   const int64_t pairs = cdiv(args.M, Cfg::BM) * cdiv(args.N, Cfg::BN);
   {
     LaunchTimer lt_(kDx ? "gemm_dx" : "gemm_fwd", st);
-    kern<<<static_cast<unsigned>(2 * pairs), Cfg::THREADS, Cfg::SMEM, st>>>(tm_act, tm_lora, args);
+    kern<<<static_cast<unsigned>(2 * pairs), Cfg::THREADS, Cfg::SMEM, st>>>(tm_act, tm_lora, args, qnf4::PairSlots{});
   }
   QLORA_CUDA_TRY(cudaGetLastError());
   return QLORA_OK;
 }
 
-// act [M, K] and lora_act [M, r] are the A operands; the output has N columns.
-int launch_gemm(bool dx, const qlora_nf4_weight* w, const uint16_t* act, int64_t M, int64_t K,
-                const uint16_t* lora_act, const uint16_t* lora_w, int r, uint16_t* out, int64_t N,
-                cudaStream_t st) {
-  CUtensorMap tm_act, tm_lora;
-  if (!make_tmap_bf16(&tm_act, act, M, K)) return QLORA_ERR_CUDA;
-  if (r == 0) tm_lora = tm_act;                  // no rank-r tail: the map is never used
-  else if (!make_tmap_bf16(&tm_lora, lora_act, M, r)) return QLORA_ERR_CUDA;
+qnf4::GemmArgs gemm_args(const qlora_nf4_weight* w, int64_t M, int64_t K, const uint16_t* lora_w, int r,
+                         uint16_t* out, int64_t N) {
   qnf4::GemmArgs a{};
   a.codes = w->codes;
   a.q8 = w->q8;
@@ -548,6 +543,18 @@ int launch_gemm(bool dx, const qlora_nf4_weight* w, const uint16_t* act, int64_t
   a.codes_32b = aligned(w->codes, 32) ? 1 : 0;
   a.L = tables().L;
   a.timeout_ns = g_timeout_ns.load();
+  return a;
+}
+
+// act [M, K] and lora_act [M, r] are the A operands; the output has N columns.
+int launch_gemm(bool dx, const qlora_nf4_weight* w, const uint16_t* act, int64_t M, int64_t K,
+                const uint16_t* lora_act, const uint16_t* lora_w, int r, uint16_t* out, int64_t N,
+                cudaStream_t st) {
+  CUtensorMap tm_act, tm_lora;
+  if (!make_tmap_bf16(&tm_act, act, M, K)) return QLORA_ERR_CUDA;
+  if (r == 0) tm_lora = tm_act;                  // no rank-r tail: the map is never used
+  else if (!make_tmap_bf16(&tm_lora, lora_act, M, r)) return QLORA_ERR_CUDA;
+  const qnf4::GemmArgs a = gemm_args(w, M, K, lora_w, r, out, N);
   const int tm = gemm_tile_m(M);
   if (tm == 512) return dx ? launch_gemm_pair<true>(a, tm_act, tm_lora, st) : launch_gemm_pair<false>(a, tm_act, tm_lora, st);
   if (!dx) {
@@ -929,14 +936,19 @@ int check_bwd_args(const uint16_t* dh, const uint16_t* x, const uint16_t* us, in
 }
 
 // ------------------------------------------------------------------ one adapter per request
-// Workspace of linear_fwd_slots: us [M, r8] bf16, the row tiles' tickets, the
-// fp32 partials of tiles cut between CTAs (one launch's, reused by the next).
+// Up to this many tokens the transposed GEMM with a persistent grid runs
+// (gemm_slots_sm100.cuh), above it the CTA-pair GEMM.
+constexpr int64_t kSlotsFewTokens = qnf4::kSgMaxN;
+// Up to this many tokens the rank-r product is one CTA per token and four
+// columns, above it the tensor-core tile (which then reads x and the adapters
+// far less often than once per token).
+constexpr int64_t kSlotsUsFew = 32;
+
+// Workspace of linear_fwd_slots: us [M, r8] bf16, and for few tokens the row
+// tiles' tickets and the fp32 partials of tiles cut between CTAs.
 struct SlotsWs {
   size_t ticket_off, part_off, total;
 };
-
-// Tokens of one launch: equal shares of at most 256.
-int64_t slots_launch_tokens(int64_t M) { return cdiv(M, cdiv(M, qnf4::kSgMaxN)); }
 
 int slots_ctas(int64_t in, int64_t out) {
   const int64_t units = cdiv(out, qnf4::kSgRows) * cdiv(in, 256);
@@ -946,8 +958,10 @@ int slots_ctas(int64_t in, int64_t out) {
 SlotsWs slots_ws(int64_t M, int64_t in, int64_t out, int r) {
   SlotsWs w{};
   w.ticket_off = round256(static_cast<size_t>(M) * padded_rank(r) * 2);
+  w.total = w.part_off = w.ticket_off;
+  if (M > kSlotsFewTokens) return w;
   w.part_off = w.ticket_off + round256(static_cast<size_t>(cdiv(out, qnf4::kSgRows)) * 4);
-  const size_t N = static_cast<size_t>(cdiv(slots_launch_tokens(M), 16) * 16);
+  const size_t N = static_cast<size_t>(cdiv(M, 16) * 16);
   w.total = w.part_off + static_cast<size_t>(slots_ctas(in, out)) * 2 * N * qnf4::kSgRows * 4;
   return w;
 }
@@ -956,10 +970,59 @@ int launch_slots_us(const uint16_t* x, const uint16_t* A, const float* scale, co
                     int64_t in, int64_t n_adapters, int r, uint16_t* us, uint32_t* tickets, int n_tickets,
                     cudaStream_t st) {
   const int r8 = padded_rank(r);
-  {
+  if (M <= kSlotsUsFew) {
     LaunchTimer lt_("slots_us", st);
     qnf4::slots_us_kernel<<<static_cast<unsigned>(M * (r8 / qnf4::kUsRanks)), qnf4::kUsThreads, 0, st>>>(
         x, A, scale, ids, in, n_adapters, r, r8, us, tickets, n_tickets);
+    QLORA_CUDA_TRY(cudaGetLastError());
+    return QLORA_OK;
+  }
+  qnf4::SlotsUsArgs a{};
+  a.scale = scale;
+  a.ids = ids;
+  a.us = us;
+  a.tickets = tickets;
+  a.n_adapters = n_adapters;
+  a.n_tickets = n_tickets;
+  a.M = static_cast<int>(M);
+  a.K = static_cast<int>(in);
+  a.r = r;
+  a.r8 = r8;
+  const int64_t most = std::min<int64_t>(n_adapters, std::min<int64_t>(M, 128));   // adapters of one token tile
+  const int per = qnf4::uu_group(r8);
+  a.groups = static_cast<int>(cdiv(most, per));
+  a.N = qnf4::uu_cols(static_cast<int>(std::min<int64_t>(most, per)), r8);
+  a.n_alloc = lr_n_alloc(a.N);
+  a.timeout_ns = g_timeout_ns.load();
+  const int64_t tiles = cdiv(M, 128), stages = cdiv(in, 64);
+  // split K while the clusters of one group per token tile fit the SMs and
+  // every CTA keeps two stages
+  int ks = 1;
+  while (ks < 8 && tiles * ks * 2 <= device_sm_count() && stages / (2 * ks) >= 2) ks *= 2;
+  a.stages_per_split = static_cast<int>(cdiv(stages, ks));
+  CUtensorMap tm_x, tm_a;
+  if (!make_tmap_bf16(&tm_x, x, static_cast<uint64_t>(M), static_cast<uint64_t>(in)) ||
+      !make_tmap_bf16(&tm_a, A, static_cast<uint64_t>(n_adapters * r), static_cast<uint64_t>(in),
+                      static_cast<uint32_t>(r8)))
+    return QLORA_ERR_CUDA;
+  if (tiles * a.groups > kMaxTokens) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  const int smem = qnf4::uu_smem_bytes(a.N);
+  QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(qnf4::slots_us_umma_kernel), smem));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.groups), static_cast<unsigned>(ks), 1);
+  cfg.blockDim = dim3(qnf4::kUuThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = static_cast<unsigned>(ks);
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ks > 1 ? 1 : 0;
+  {
+    LaunchTimer lt_("slots_us", st);
+    QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, qnf4::slots_us_umma_kernel, tm_x, tm_a, a));
   }
   QLORA_CUDA_TRY(cudaGetLastError());
   return QLORA_OK;
@@ -972,64 +1035,73 @@ int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* 
   const SlotsWs ws = slots_ws(M, in, out, r);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   uint16_t* us = reinterpret_cast<uint16_t*>(base);
-  uint32_t* tickets = reinterpret_cast<uint32_t*>(base + ws.ticket_off);
-  const int row_tiles = static_cast<int>(cdiv(out, qnf4::kSgRows));
   const int r8 = padded_rank(r);
-  const int64_t step = slots_launch_tokens(M);
-  CUtensorMap tm_codes;
-  if (!make_tmap_codes(&tm_codes, w->codes, static_cast<uint64_t>(out), static_cast<uint64_t>(in / 2), qnf4::kSgRows))
-    return QLORA_ERR_CUDA;
-  for (int64_t m0 = 0; m0 < M; m0 += step) {
-    const int64_t m = std::min(step, M - m0);
-    const int rc = launch_slots_us(x + m0 * in, A, scale, ids + m0, m, in, n_adapters, r, us + m0 * r8, tickets,
-                                   row_tiles, st);
-    if (rc != QLORA_OK) return rc;
-    qnf4::SlotsGemmArgs a{};
-    a.q8 = w->q8;
-    a.step2 = w->step2;
-    a.mean = w->mean;
-    a.us = us + m0 * r8;
-    a.B = B;
-    a.ids = ids + m0;
-    a.h = h + m0 * out;
-    a.part = reinterpret_cast<float*>(base + ws.part_off);
-    a.tickets = tickets;
-    a.n_adapters = n_adapters;
-    a.M = static_cast<int>(m);
-    a.out = static_cast<int>(out);
-    a.K = static_cast<int>(in);
-    a.r = r;
-    a.r8 = r8;
-    a.N = static_cast<int>(cdiv(m, 16) * 16);
-    a.L = tables().L;
-    a.timeout_ns = g_timeout_ns.load();
-    CUtensorMap tm_x;
-    if (!make_tmap_bf16_blocks(&tm_x, x + m0 * in, static_cast<uint64_t>(m), static_cast<uint64_t>(in),
-                               static_cast<uint32_t>(a.N), static_cast<uint32_t>(qnf4::sg_kb(a.N))))
-      return QLORA_ERR_CUDA;
-    const auto kern = a.N <= 32    ? qnf4::slots_gemm_kernel<4, 4, true>
-                      : a.N <= 64  ? qnf4::slots_gemm_kernel<4, 2, true>
-                      : a.N <= 128 ? qnf4::slots_gemm_kernel<2, 2, true>
-                                   : qnf4::slots_gemm_kernel<2, 2, false>;
-    const int smem = qnf4::sg_smem_bytes(a.N);
-    QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), smem));
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(slots_ctas(in, out)));
-    cfg.blockDim = dim3(qnf4::kSgThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    // may start while the rank-r kernel runs; it waits for it before it reads us or the tickets
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = g_timing_on.load() ? 0 : 1;               // (timed launches one after another)
+  const bool few = M <= kSlotsFewTokens;
+  uint32_t* tickets = few ? reinterpret_cast<uint32_t*>(base + ws.ticket_off) : nullptr;
+  const int rc = launch_slots_us(x, A, scale, ids, M, in, n_adapters, r, us, tickets,
+                                 few ? static_cast<int>(cdiv(out, qnf4::kSgRows)) : 0, st);
+  if (rc != QLORA_OK) return rc;
+  if (!few) {
+    using Cfg = qnf4::PairCfg;
+    CUtensorMap tm_act;
+    if (!make_tmap_bf16(&tm_act, x, static_cast<uint64_t>(M), static_cast<uint64_t>(in))) return QLORA_ERR_CUDA;
+    const auto kern = qnf4::qlora_gemm_pair_kernel<false, true>;
+    QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), Cfg::SLOTS_SMEM));
+    const int64_t pairs = cdiv(M, Cfg::BM) * cdiv(out, Cfg::BN);
     {
       LaunchTimer lt_("slots_gemm", st);
-      QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, tm_codes, tm_x, a));
+      kern<<<static_cast<unsigned>(2 * pairs), Cfg::THREADS, Cfg::SLOTS_SMEM, st>>>(
+          tm_act, tm_act, gemm_args(w, M, in, B, r, h, out), qnf4::PairSlots{ids, us, n_adapters, r8});
     }
     QLORA_CUDA_TRY(cudaGetLastError());
+    return QLORA_OK;
   }
+  qnf4::SlotsGemmArgs a{};
+  a.q8 = w->q8;
+  a.step2 = w->step2;
+  a.mean = w->mean;
+  a.us = us;
+  a.B = B;
+  a.ids = ids;
+  a.h = h;
+  a.part = reinterpret_cast<float*>(base + ws.part_off);
+  a.tickets = tickets;
+  a.n_adapters = n_adapters;
+  a.M = static_cast<int>(M);
+  a.out = static_cast<int>(out);
+  a.K = static_cast<int>(in);
+  a.r = r;
+  a.r8 = r8;
+  a.N = static_cast<int>(cdiv(M, 16) * 16);
+  a.L = tables().L;
+  a.timeout_ns = g_timeout_ns.load();
+  CUtensorMap tm_codes, tm_x;
+  if (!make_tmap_codes(&tm_codes, w->codes, static_cast<uint64_t>(out), static_cast<uint64_t>(in / 2), qnf4::kSgRows) ||
+      !make_tmap_bf16_blocks(&tm_x, x, static_cast<uint64_t>(M), static_cast<uint64_t>(in),
+                             static_cast<uint32_t>(a.N), static_cast<uint32_t>(qnf4::sg_kb(a.N))))
+    return QLORA_ERR_CUDA;
+  const auto kern = a.N <= 32    ? qnf4::slots_gemm_kernel<4, 4, true>
+                    : a.N <= 64  ? qnf4::slots_gemm_kernel<4, 2, true>
+                    : a.N <= 128 ? qnf4::slots_gemm_kernel<2, 2, true>
+                                 : qnf4::slots_gemm_kernel<2, 2, false>;
+  const int smem = qnf4::sg_smem_bytes(a.N);
+  QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), smem));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(slots_ctas(in, out)));
+  cfg.blockDim = dim3(qnf4::kSgThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  // may start while the rank-r kernel runs; it waits for it before it reads us or the tickets
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = g_timing_on.load() ? 0 : 1;               // (timed launches one after another)
+  {
+    LaunchTimer lt_("slots_gemm", st);
+    QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, tm_codes, tm_x, a));
+  }
+  QLORA_CUDA_TRY(cudaGetLastError());
   return QLORA_OK;
 }
 

@@ -28,10 +28,22 @@
 // commits each stage with a multicast arrive on both CTAs' "empty" barriers,
 // and the end of the accumulation on both "acc_full".
 // Every wait is bounded (see gemm_sm100.cuh); no TMA multicast is used.
+//
+// kSlots: the forward with one adapter per token (h[m] = W0 x[m] + B_a us[m],
+// a = ids[m]).  The CTAs list the distinct adapters of their 512 tokens; the
+// rank columns of the listed adapters, one after another, are the K slices
+// behind the base's.  There the dequant groups write both operands: B_a rows
+// as they are, and the token rows of us under the columns of the token's own
+// adapter with zeros elsewhere.  A B value that is infinite or NaN would reach
+// the other tokens through those zeros: it is carried as 0 and both CTAs are
+// marked, and the epilogue adds its products to the adapter's own tokens.
+// Prompts of few requests cost a slice or two this way, against a second pass
+// over h (M out 4 bytes) for adding the adapters behind the GEMM.
 #pragma once
 
 #include "common.cuh"
 #include "gemm_sm100.cuh"
+#include "slots.cuh"
 
 namespace qnf4 {
 
@@ -47,13 +59,22 @@ struct PairCfg {
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int kGroups = 4;                    // dequant groups, one stage each in turn
   static constexpr int THREADS = 64 + kGroups * 128;   // 2 + 16 warps
+  // kSlots: per token its first rank column, the distinct adapters, counts
+  static constexpr int SLOTS_SMEM = SMEM + (2 * BM + 16) * 4;
 };
 
-template <bool kDx>
+struct PairSlots {
+  const int32_t* ids;       // [M]
+  const uint16_t* us;       // [M, r8]
+  int64_t n_adapters;
+  int r8;                   // r rounded up to 8
+};
+
+template <bool kDx, bool kSlots = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
 qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
                        const __grid_constant__ CUtensorMap tm_lora,
-                       const GemmArgs args) {
+                       const GemmArgs args, const PairSlots slots) {
   using Cfg = PairCfg;
   constexpr int kStages = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -82,9 +103,29 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
   const int n0 = tile_n * Cfg::BN;
   const int n0_half = n0 + 128 * static_cast<int>(rank);
   const int n_main = args.K / 64;
-  const int n_lora = (args.r + 63) / 64;
-  const int n_iter = n_main + n_lora;
   const uint64_t tmo = args.timeout_ns;
+  int32_t* tok_col = reinterpret_cast<int32_t*>(smem + Cfg::RING + 256);   // kSlots
+  int32_t* list = tok_col + Cfg::BM;
+  volatile int32_t* odd = list + Cfg::BM + 15;         // a B value of either CTA was not finite
+  int k_low = args.r;                                  // rank columns behind the base
+  int n_list = 0;
+  if constexpr (kSlots) {
+    int32_t id = -1;
+    if (threadIdx.x < Cfg::BM && m0 + static_cast<int>(threadIdx.x) < args.M) {
+      id = __ldg(slots.ids + m0 + threadIdx.x);
+      if (id < 0 || id >= slots.n_adapters) id = -1;
+    }
+    int place;
+    // 16 counts: the list has room for 512, the counts lie behind it
+    __shared__ int32_t counts[Cfg::BM / 32];
+    n_list = distinct_slots<Cfg::BM, 2 * Cfg::BM>(id, reinterpret_cast<int32_t*>(smem), list, counts, place);
+    if (threadIdx.x < Cfg::BM) tok_col[threadIdx.x] = place < 0 ? -(1 << 29) : place * slots.r8;
+    if (threadIdx.x == 0) *odd = 0;
+    k_low = n_list * slots.r8;
+    fence_proxy_async_smem();                          // the hash table before the copies over it
+  }
+  const int n_lora = (k_low + 63) / 64;
+  const int n_iter = n_main + n_lora;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -126,6 +167,11 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
         const uint32_t ph = (it / kStages) & 1u;
         wait(empty + s, ph ^ 1u);
         if (*abort_flag) break;                           // a wait timed out: issue nothing more
+        if (kSlots && it >= n_main) {                     // the dequant groups write the token operand
+          if (leader) mbar_arrive(full + s);
+          ++issued;
+          continue;
+        }
         if (leader) mbar_arrive_expect_tx(full + s, 2 * Cfg::A_STAGE);    // both CTAs' bytes
         const uint32_t bar = mapa_shared(smem_u32(full + s), 0);
         const uint32_t dst = smem_u32(a_ring + s * Cfg::A_STAGE);
@@ -162,7 +208,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
         const uint32_t a_base = smem_u32(a_ring + s * Cfg::A_STAGE);
         const uint32_t b_base = smem_u32(b_ring + s * Cfg::B_STAGE);
         int ksteps = 4;
-        if (it >= n_main) ksteps = min(4, (args.r - (it - n_main) * 64 + 15) / 16);
+        if (it >= n_main) ksteps = min(4, (k_low - (it - n_main) * 64 + 15) / 16);
         for (int kk = 0; kk < ksteps; ++kk) {
           const uint64_t bdesc = kDx ? umma_desc_sw128(b_base + kk * 2048, 8192, 1024)
                                      : umma_desc_sw128(b_base + kk * 32, 16, 1024);
@@ -251,6 +297,43 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
 #pragma unroll
           for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
         }
+      } else if constexpr (kSlots) {
+        // rank columns [64 j, 64 j + 64) of the listed adapters, in chunks of 8
+        const int j = it - n_main;
+        int li = j * 64 / slots.r8, c0 = j * 64 - li * slots.r8;
+        uint32_t exps = 0;                                // bit 15 or 31: an exponent of all ones
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          v[c] = make_uint4(0, 0, 0, 0);
+          if (col_valid && li < n_list) {
+            const uint16_t* src = args.lora_w + (static_cast<int64_t>(list[li]) * args.N + lora_row) * args.r + c0;
+            if ((args.r & 7) == 0) {
+              v[c] = ld_nc_v4(src);
+            } else {
+              uint32_t w[4] = {0, 0, 0, 0};
+              for (int i = 0; i < 8; ++i)
+                if (c0 + i < args.r) w[i >> 1] |= static_cast<uint32_t>(__ldg(src + i)) << (16 * (i & 1));
+              v[c] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          c0 += 8;
+          if (c0 == slots.r8) { c0 = 0; ++li; }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          exps |= ((v[c].x & 0x7F807F80u) + 0x00800080u) | ((v[c].y & 0x7F807F80u) + 0x00800080u) |
+                  ((v[c].z & 0x7F807F80u) + 0x00800080u) | ((v[c].w & 0x7F807F80u) + 0x00800080u);
+        if (exps & 0x80008000u) {
+          auto finite = [](uint32_t& w) {
+            if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+            if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+          };
+#pragma unroll
+          for (int c = 0; c < 8; ++c) { finite(v[c].x); finite(v[c].y); finite(v[c].z); finite(v[c].w); }
+          const uint32_t at = smem_u32(const_cast<int32_t*>(odd));
+          for (uint32_t k = 0; k < 2; ++k)                // before this warp's arrive on "full"
+            asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(mapa_shared(at, k)), "r"(1) : "memory");
+        }
       } else {
         const int j = it - n_main;
         const uint16_t* src = nullptr;
@@ -292,6 +375,26 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
       wait(empty + s, ph ^ 1u);
 #pragma unroll
       for (int c = 0; c < 8; ++c) sts_v4(dst + ((c ^ key) << 4), v[c].x, v[c].y, v[c].z, v[c].w);
+      if constexpr (kSlots) {
+        if (it >= n_main) {
+          // token rows t of both sub-tiles: us under the columns of the token's adapter
+          const int e = it - n_main;
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
+            const int i = sub * 256 + static_cast<int>(rank) * 128 + t;         // of the 512 tokens
+            const uint32_t row = smem_u32(a_ring + s * Cfg::A_STAGE) + sub * Cfg::A_SUB + t * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) sts_v4(row + ((c ^ (t & 7)) << 4), 0, 0, 0, 0);
+            const int col = tok_col[i] - e * 64;
+            const uint16_t* src = slots.us + static_cast<int64_t>(m0 + i) * slots.r8;
+#pragma unroll 2
+            for (int j = max(0, -col); j < slots.r8 && col + j < 64; j += 8) {
+              const uint4 u = *reinterpret_cast<const uint4*>(src + j);
+              sts_v4(row + ((((col + j) >> 3) ^ (t & 7)) << 4), u.x, u.y, u.z, u.w);
+            }
+          }
+        }
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (warp_lead) mbar_arrive_remote(mapa_shared(smem_u32(full + s), 0));
@@ -311,6 +414,20 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
       uint32_t v[32];
       tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + sub * 256 + col, v);
       tmem_ld_wait();
+      if constexpr (kSlots) {
+        const int c = tok_col[m - m0];
+        if (*odd && m < args.M && n0 + col < args.N && c >= 0) {
+          const int64_t a = list[c / slots.r8];
+#pragma unroll 1
+          for (int i = 0; i < 32; ++i) {
+            const float f = slots_odd_term(args.lora_w + (a * args.N + n0 + col + i) * args.r,
+                                           slots.us + static_cast<int64_t>(m) * slots.r8, args.r);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)                  // (constant indices keep v in registers)
+              if (k == i) v[k] = __float_as_uint(__uint_as_float(v[k]) + f);
+          }
+        }
+      }
       if (m < args.M && n0 + col < args.N) {
         uint16_t* dstp = args.out + static_cast<int64_t>(m) * args.N + n0 + col;
 #pragma unroll

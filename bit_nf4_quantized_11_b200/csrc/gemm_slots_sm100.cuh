@@ -50,6 +50,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "slots.cuh"
 
 namespace qnf4 {
 
@@ -179,17 +180,6 @@ __device__ __forceinline__ void lds_v4(uint32_t addr, uint32_t (&v)[4]) {
 
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The products of an adapter row's infinite or NaN B values with a token's us.
-__device__ __noinline__ float slots_odd_term(const uint16_t* B_row, const uint16_t* us, int r) {
-  float f = 0.f;
-  for (int j = 0; j < r; ++j) {
-    const uint32_t b = __ldg(B_row + j);
-    if ((b & 0x7F80u) == 0x7F80u)
-      f = fmaf(__uint_as_float(static_cast<uint32_t>(us[j]) << 16), __uint_as_float(b << 16), f);
-  }
-  return f;
-}
-
 // First unit of CTA c when T units are dealt out to G CTAs.
 __device__ __forceinline__ int64_t sg_unit_begin(int64_t c, int64_t T, int64_t G) { return T * c / G; }
 
@@ -260,15 +250,8 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
     tmem_alloc(tmem_holder, kSgTmemCols);
     tmem_relinquish();
   }
-  // The tokens' slots (-1: no adapter, or past the batch), and the distinct
-  // ones in order of first appearance: a hash table over the code ring, which
-  // is not in use yet, keeps each slot's first token.
-  int32_t* h_key = reinterpret_cast<int32_t*>(c_ring);
-  int32_t* h_first = h_key + kSgHash;
-  for (int i = threadIdx.x; i < kSgHash; i += kSgThreads) {
-    h_key[i] = -1;
-    h_first[i] = kSgMaxN;
-  }
+  // The tokens' slots (-1: no adapter, or past the batch) and the distinct
+  // ones; the hash table lies over the code ring, which is not in use yet.
   int32_t my_id = -1;
   if (threadIdx.x < kSgMaxN && static_cast<int>(threadIdx.x) < args.M) {
     my_id = __ldg(args.ids + threadIdx.x);
@@ -282,35 +265,10 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  int slot = -1;                                             // the token's place in the hash table
-  if (my_id >= 0) {
-    slot = static_cast<int>((static_cast<uint32_t>(my_id) * 2654435761u) >> 23);   // 9 bits
-    while (true) {
-      const int32_t was = atomicCAS(h_key + slot, -1, my_id);
-      if (was == -1 || was == my_id) break;
-      slot = (slot + 1) & (kSgHash - 1);                     // at most 256 of 512 places are taken
-    }
-    atomicMin(h_first + slot, static_cast<int32_t>(threadIdx.x));
-  }
-  __syncthreads();
-  const bool leader = slot >= 0 && h_first[slot] == static_cast<int32_t>(threadIdx.x);
-  const uint32_t lead = __ballot_sync(0xFFFFFFFFu, leader);
-  if (warp < kSgMaxN / 32 && lane == 0) counts[warp] = __popc(lead);
-  __syncthreads();
-  int n_list = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < kSgMaxN / 32; ++w) {
-    const int c = counts[w];
-    if (w < warp) before += c;
-    n_list += c;
-  }
-  if (leader) {
-    const int li = before + __popc(lead & ((1u << lane) - 1u));
-    list[li] = my_id;
-    h_key[slot] = li;                                        // (the keys are not needed any more)
-  }
-  __syncthreads();
-  if (threadIdx.x < kSgMaxN) tok_col[threadIdx.x] = slot < 0 ? -(1 << 29) : h_key[slot] * args.r8;
+  int place;
+  const int n_list =
+      distinct_slots<kSgMaxN, kSgHash>(my_id, reinterpret_cast<int32_t*>(c_ring), list, counts, place);
+  if (threadIdx.x < kSgMaxN) tok_col[threadIdx.x] = place < 0 ? -(1 << 29) : place * args.r8;
   fence_proxy_async_smem();                                  // the table's words before the copies over them
   __syncthreads();
   const uint32_t tmem_base = *tmem_holder;

@@ -90,6 +90,67 @@ __global__ void __launch_bounds__(kTsThreads) token_slots_kernel(const int32_t* 
   }
 }
 
+// ---------------------------------------------------------------------------
+// The distinct adapters of a tile of tokens, in order of first appearance.
+// Thread t holds token t's slot (-1: none); all threads of the CTA take part,
+// kTok of them with a token (a multiple of 32).  A hash table (2 * kHash
+// ints, kHash >= 2 kTok a power of two) keeps each slot's first token.
+// list: the distinct slots; the return value is how many; `place` is the
+// token's index into the list, -1 for none.  counts: kTok / 32 ints.
+template <int kTok, int kHash>
+__device__ __forceinline__ int distinct_slots(int32_t id, int32_t* hash, int32_t* list, int32_t* counts, int& place) {
+  static_assert(kHash >= 2 * kTok && (kHash & (kHash - 1)) == 0, "half-empty power-of-two table");
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  int32_t* key = hash;
+  int32_t* first = hash + kHash;
+  for (int i = t; i < kHash; i += static_cast<int>(blockDim.x)) {
+    key[i] = -1;
+    first[i] = kTok;
+  }
+  __syncthreads();
+  int at = -1;
+  if (t < kTok && id >= 0) {
+    at = static_cast<int>((static_cast<uint32_t>(id) * 2654435761u) >> 16) & (kHash - 1);
+    while (true) {                                           // ends: half of the places stay free
+      const int32_t was = atomicCAS(key + at, -1, id);
+      if (was == -1 || was == id) break;
+      at = (at + 1) & (kHash - 1);
+    }
+    atomicMin(first + at, t);
+  }
+  __syncthreads();
+  const bool leader = at >= 0 && first[at] == t;
+  const uint32_t lead = __ballot_sync(0xFFFFFFFFu, leader);
+  if (warp < kTok / 32 && lane == 0) counts[warp] = __popc(lead);
+  __syncthreads();
+  int n = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kTok / 32; ++w) {
+    const int c = counts[w];
+    if (w < warp) before += c;
+    n += c;
+  }
+  if (leader) {
+    const int li = before + __popc(lead & ((1u << lane) - 1u));
+    list[li] = id;
+    key[at] = li;                                            // (nobody looks keys up any more)
+  }
+  __syncthreads();
+  place = at < 0 ? -1 : key[at];
+  return n;
+}
+
+// The products of an adapter row's infinite or NaN B values with a token's us.
+__device__ __noinline__ float slots_odd_term(const uint16_t* B_row, const uint16_t* us, int r) {
+  float f = 0.f;
+  for (int j = 0; j < r; ++j) {
+    const uint32_t b = __ldg(B_row + j);
+    if ((b & 0x7F80u) == 0x7F80u)
+      f = fmaf(__uint_as_float(static_cast<uint32_t>(us[j]) << 16), __uint_as_float(b << 16), f);
+  }
+  return f;
+}
+
 // us of a few tokens.  One CTA per (token, 4 rank columns): its warps share
 // the K axis (thread t takes the 8-column chunks t, t + 256, ...), then add up
 // over a butterfly and shared memory in warp order.  us has rows of r8 = r
