@@ -16,6 +16,9 @@ Entry points (same names as the C ABI, without the ``qlora_`` prefix):
   linear_fwd_group(problems), linear_bwd_group(problems)   (n projections issued together)
   token_slots(lengths, slots, n_tokens)           -> ids (the adapter slot of every token)
   linear_fwd_slots(x, w, A, B, scale, ids)        -> h   (one adapter per request over a shared base)
+  dropout_keep_bits(rng, p, M, n)                 -> keep bits of the counter-based LoRA dropout
+  linear_fwd_dropout_rng(x, w, A, B, alpha, rng, p)         -> (h, us)   (that mask, never stored)
+  linear_bwd_dropout_rng(dh, x, us, w, A, B, alpha, rng, p) -> (dx, dA, dB)
   workspace_size(op, M, in_features, out_features, r)
   last_device_status(), set_wait_timeout_ns(ns), selftest_wait_timeout()
 """
@@ -39,6 +42,8 @@ __all__ = [
     "quantize_codebook", "dequantize_codebook", "CODEBOOK_NF4", "CODEBOOK_INT4",
     "linear_fwd_dropout", "linear_bwd_dropout", "pack_keep_mask", "OP_LINEAR_FWD_DROPOUT", "OP_LINEAR_BWD_DROPOUT",
     "token_slots", "linear_fwd_slots", "OP_LINEAR_FWD_SLOTS",
+    "dropout_keep_bits", "linear_fwd_dropout_rng", "linear_bwd_dropout_rng",
+    "OP_LINEAR_FWD_DROPOUT_RNG", "OP_LINEAR_BWD_DROPOUT_RNG",
     "OP_QUANTIZE", "OP_DEQUANTIZE", "OP_LINEAR_FWD", "OP_LINEAR_BWD",
     "quantize_shard_plan", "quantize_shard_workspace_size", "quantize_nf4_shard_local", "quantize_nf4_shard_finish",
 ]
@@ -109,6 +114,9 @@ def load():
         "qlora_dequantize_codebook": (I, [I, W, P, P]),
         "qlora_linear_fwd_dropout": (I, [P, I64, W, P, P, I, F, P, F, P, P, P, SZ, P]),
         "qlora_linear_bwd_dropout": (I, [P, P, P, I64, W, P, P, I, F, P, F, P, P, P, P, SZ, P]),
+        "qlora_dropout_keep_bits": (I, [P, ctypes.c_double, I64, I64, P, P]),
+        "qlora_linear_fwd_dropout_rng": (I, [P, I64, W, P, P, I, F, P, ctypes.c_double, P, P, P, SZ, P]),
+        "qlora_linear_bwd_dropout_rng": (I, [P, P, P, I64, W, P, P, I, F, P, ctypes.c_double, P, P, P, P, SZ, P]),
         "qlora_token_slots": (I, [P, P, I64, I64, P, P]),
         "qlora_linear_fwd_slots": (I, [P, I64, W, P, P, I64, I, P, P, P, P, SZ, P]),
         "qlora_quantize_shard_plan": (I, [I64, I, I, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64),
@@ -543,6 +551,70 @@ def linear_bwd_dropout(dh, x, us, w: NF4Weight, A, B, alpha: float, keep_bits, p
     return dx, dA, dB
 
 
+OP_LINEAR_FWD_DROPOUT_RNG, OP_LINEAR_BWD_DROPOUT_RNG = 7, 8
+
+
+def dropout_keep_bits(rng, p: float, M: int, n: int, out=None) -> torch.Tensor:
+    """The keep mask of the counter-based LoRA dropout as bits, uint8 [M, n/8]
+    (the layout of :func:`pack_keep_mask`); rng int64 [2] = (seed, offset) on
+    the device."""
+    dev = torch.cuda.current_device()
+    bits = out if out is not None else torch.empty((M, n // 8), dtype=torch.uint8, device=dev)
+    _ready(dev, (rng, torch.int64, "rng", (2,)), (bits, torch.uint8, "out", (M, n // 8)))
+    _check(load().qlora_dropout_keep_bits(rng.data_ptr(), p, M, n, bits.data_ptr(), _raw_stream(dev)),
+           "qlora_dropout_keep_bits")
+    return bits
+
+
+def linear_fwd_dropout_rng(x, w: NF4Weight, A, B, alpha: float, rng, p: float, h=None, us=None, workspace=None):
+    """:func:`linear_fwd_dropout` with a mask that is drawn where it is used
+    and never stored: a function of rng = int64 [2] (seed, offset) on the
+    device, read when the kernels run, and of the value's place.  p is rounded
+    to a multiple of 2**-16."""
+    dev = torch.cuda.current_device()
+    M, r = x.shape[0], A.shape[0]
+    rows, cols = w.rows, w.cols
+    h = h if h is not None else torch.empty((M, rows), dtype=torch.bfloat16, device=dev)
+    us = us if us is not None else torch.empty((M, r), dtype=torch.bfloat16, device=dev)
+    _ready(dev, (x, torch.bfloat16, "x", (M, cols)), (A, torch.bfloat16, "A", (r, cols)),
+           (B, torch.bfloat16, "B", (rows, r)), (rng, torch.int64, "rng", (2,)),
+           (h, torch.bfloat16, "h", (M, rows)), (us, torch.bfloat16, "us", (M, r)),
+           (w.codes, torch.uint8, "w.codes", (rows, cols // 2)))
+    ws = _workspace(_cached_workspace_size(OP_LINEAR_FWD_DROPOUT_RNG, M, cols, rows, r, dev), x.device, workspace)
+    cw = w._c()
+    _check(load().qlora_linear_fwd_dropout_rng(x.data_ptr(), M, ctypes.byref(cw), A.data_ptr(), B.data_ptr(), r, alpha,
+                                               rng.data_ptr(), p, h.data_ptr(), us.data_ptr(),
+                                               ws.data_ptr() if ws is not None else None,
+                                               ws.numel() if ws is not None else 0, _raw_stream(dev)),
+           "qlora_linear_fwd_dropout_rng")
+    return h, us
+
+
+def linear_bwd_dropout_rng(dh, x, us, w: NF4Weight, A, B, alpha: float, rng, p: float, dx=None, dA=None, dB=None,
+                           workspace=None):
+    """Backward of :func:`linear_fwd_dropout_rng`; rng must hold what it held
+    in the forward."""
+    dev = torch.cuda.current_device()
+    M, r = x.shape[0], A.shape[0]
+    rows, cols = w.rows, w.cols
+    dx = dx if dx is not None else torch.empty((M, cols), dtype=torch.bfloat16, device=dev)
+    dA = dA if dA is not None else torch.empty((r, cols), dtype=torch.float32, device=dev)
+    dB = dB if dB is not None else torch.empty((rows, r), dtype=torch.float32, device=dev)
+    _ready(dev, (dh, torch.bfloat16, "dh", (M, rows)), (x, torch.bfloat16, "x", (M, cols)),
+           (us, torch.bfloat16, "us", (M, r)), (A, torch.bfloat16, "A", (r, cols)),
+           (B, torch.bfloat16, "B", (rows, r)), (rng, torch.int64, "rng", (2,)),
+           (dx, torch.bfloat16, "dx", (M, cols)), (dA, torch.float32, "dA", (r, cols)),
+           (dB, torch.float32, "dB", (rows, r)), (w.codes, torch.uint8, "w.codes", (rows, cols // 2)))
+    ws = _workspace(_cached_workspace_size(OP_LINEAR_BWD_DROPOUT_RNG, M, cols, rows, r, dev), x.device, workspace)
+    cw = w._c()
+    _check(load().qlora_linear_bwd_dropout_rng(dh.data_ptr(), x.data_ptr(), us.data_ptr(), M, ctypes.byref(cw),
+                                               A.data_ptr(), B.data_ptr(), r, alpha, rng.data_ptr(), p, dx.data_ptr(),
+                                               dA.data_ptr(), dB.data_ptr(), ws.data_ptr() if ws is not None else None,
+                                               ws.numel() if ws is not None else 0, _raw_stream(dev)),
+           "qlora_linear_bwd_dropout_rng")
+    return dx, dA, dB
+
+
 OP_LINEAR_FWD_SLOTS = 6
 
 
@@ -598,7 +670,8 @@ def selftest_wait_timeout() -> int:
 
 KERNEL_NAMES = ("quantize_blocks", "scale_mean_tree", "dq_scales", "dequantize", "gemm_fwd", "gemm_dx",
                 "gemv", "gemv_finalize", "lora_rowwise", "lora_rowwise_du", "lora_colwise",
-                "merge_adapter", "dropout_dx", "lora_fewtok", "lora_pad", "token_slots", "slots_us", "slots_gemm")
+                "merge_adapter", "dropout_dx", "lora_fewtok", "lora_pad", "token_slots", "slots_us", "slots_gemm",
+                "keep_bits")
 
 
 def timing_enable(on: bool = True) -> bool:

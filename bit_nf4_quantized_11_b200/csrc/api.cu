@@ -593,15 +593,17 @@ LrShape lr_shape(int64_t tiles, int64_t stages, int N, bool b_mn_major) {
   return sh;
 }
 
-template <bool kCol, bool kBMN>
+template <bool kCol, bool kBMN, bool kRng = false>
 int launch_lora_umma(const CUtensorMap (&tm)[4], const qnf4::LrArgs& a, int ks, unsigned grid_x, const char* name,
                      cudaStream_t st) {
-  auto kern = qnf4::lora_umma_kernel<kCol, kBMN>;
-  const int smem = qnf4::lr_smem_bytes(a.N, kBMN, a.ring);
+  auto kern = qnf4::lora_umma_kernel<kCol, kBMN, kRng>;
+  int smem = qnf4::lr_smem_bytes(a.N, kBMN, a.ring);
+  // with all of the tensor memory, no other rank-r CTA (72 KB or more) beside it
+  if (kRng && a.n_alloc == 512) smem = std::max(smem, 160 * 1024);
   QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), smem));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid_x, static_cast<unsigned>(ks), 1);
-  const bool masked = a.p[0].keep != nullptr || a.p[1].keep != nullptr;
+  const bool masked = kRng ? a.p[0].masked || a.p[1].masked : a.p[0].keep != nullptr || a.p[1].keep != nullptr;
   cfg.blockDim = dim3(masked ? qnf4::kLrMaskThreads : qnf4::kLrThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -761,10 +763,10 @@ int linear_fwd_impl(const uint16_t* x, const uint8_t* keep, int64_t M, const qlo
     LaunchTimer lt_("lora_fewtok", st);
     if (M > 8)
       qnf4::fewtok_us_kernel<16><<<chunks, qnf4::kFtThreads, 0, st>>>(x, keep, A, static_cast<int>(M), in, r, s_lora,
-                                                                      ft_part, ticket, us_out);
+                                                                      ft_part, ticket, us_out, qnf4::DropoutRng{});
     else
       qnf4::fewtok_us_kernel<8><<<chunks, qnf4::kFtThreads, 0, st>>>(x, keep, A, static_cast<int>(M), in, r, s_lora,
-                                                                     ft_part, ticket, us_out);
+                                                                     ft_part, ticket, us_out, qnf4::DropoutRng{});
   } else {
     rc = launch_rowwise<false>(x, A, us_out, M, in, r, s_lora, st, keep);    // us = bf16(s (x k) A^T)
   }
@@ -867,12 +869,12 @@ int linear_bwd_impl(const uint16_t* dh, const uint16_t* x, const uint16_t* us, i
   if (rc == QLORA_OK) {
     const int64_t tiles = cdiv(M, qnf4::kDxTileRows) * cdiv(in, qnf4::kDxTileCols);
     const int smem = qnf4::dx_smem_bytes(r);
-    if (set_max_smem(reinterpret_cast<const void*>(qnf4::dropout_dx_kernel), smem) != cudaSuccess) {
+    if (set_max_smem(reinterpret_cast<const void*>(qnf4::dropout_dx_kernel<false>), smem) != cudaSuccess) {
       rc = QLORA_ERR_CUDA;
     } else {
       LaunchTimer lt_("dropout_dx", g.hi);
-      qnf4::dropout_dx_kernel<<<static_cast<unsigned>(tiles), qnf4::kDxThreads, smem, g.hi>>>(
-          dx, du, A, keep, M, in, r, inv_keep);                                           // + (du A) k/(1-p)
+      qnf4::dropout_dx_kernel<false><<<static_cast<unsigned>(tiles), qnf4::kDxThreads, smem, g.hi>>>(
+          dx, du, A, keep, M, in, r, inv_keep, qnf4::DropoutRng{});                       // + (du A) k/(1-p)
       if (cudaGetLastError() != cudaSuccess) rc = QLORA_ERR_CUDA;
     }
   }
@@ -939,10 +941,15 @@ int check_bwd_args(const uint16_t* dh, const uint16_t* x, const uint16_t* us, in
 // Up to this many tokens the transposed GEMM with a persistent grid runs
 // (gemm_slots_sm100.cuh), above it the CTA-pair GEMM.
 constexpr int64_t kSlotsFewTokens = qnf4::kSgMaxN;
-// Up to this many tokens the rank-r product is one CTA per token and four
-// columns, above it the tensor-core tile (which then reads x and the adapters
-// far less often than once per token).
-constexpr int64_t kSlotsUsFew = 32;
+// The rank-r product takes one CTA per token and four columns while that reads
+// about what it must: few tokens, or adapters that differ from token to token.
+// Otherwise the tensor-core tile, which reads an adapter once per 128 tokens.
+// Measured, one CTA per token / tile: 64 tokens of 64 adapters, 8192 wide,
+// rank 16: 14 / 18 us; 256 tokens of 256 adapters, 4096, rank 16: 17 / 37 us;
+// 256 tokens of 2 adapters, 4096, rank 64: 24 / 14 us.
+bool slots_us_per_token(int64_t M, int64_t n_adapters, int r8) {
+  return M <= kSlotsFewTokens && (M * r8 < 4096 || 16 * n_adapters >= M);
+}
 
 // Workspace of linear_fwd_slots: us [M, r8] bf16, and for few tokens the row
 // tiles' tickets and the fp32 partials of tiles cut between CTAs.
@@ -970,7 +977,7 @@ int launch_slots_us(const uint16_t* x, const uint16_t* A, const float* scale, co
                     int64_t in, int64_t n_adapters, int r, uint16_t* us, uint32_t* tickets, int n_tickets,
                     cudaStream_t st) {
   const int r8 = padded_rank(r);
-  if (M <= kSlotsUsFew) {
+  if (slots_us_per_token(M, n_adapters, r8)) {
     LaunchTimer lt_("slots_us", st);
     qnf4::slots_us_kernel<<<static_cast<unsigned>(M * (r8 / qnf4::kUsRanks)), qnf4::kUsThreads, 0, st>>>(
         x, A, scale, ids, in, n_adapters, r, r8, us, tickets, n_tickets);
@@ -989,12 +996,15 @@ int launch_slots_us(const uint16_t* x, const uint16_t* A, const float* scale, co
   a.r = r;
   a.r8 = r8;
   const int64_t most = std::min<int64_t>(n_adapters, std::min<int64_t>(M, 128));   // adapters of one token tile
-  const int per = qnf4::uu_group(r8);
-  a.groups = static_cast<int>(cdiv(most, per));
-  a.N = qnf4::uu_cols(static_cast<int>(std::min<int64_t>(most, per)), r8);
+  const int64_t tiles = cdiv(M, 128), stages = cdiv(in, 64);
+  // as many adapters per group as the UMMA takes, or fewer (64 columns at
+  // least) while the groups of different adapters leave SMs without work
+  a.per = static_cast<int>(std::min<int64_t>(most, 256 / r8));
+  while (a.per > 1 && a.per * r8 > 64 && tiles * cdiv(most, a.per) * 8 < device_sm_count()) a.per = (a.per + 1) / 2;
+  a.groups = static_cast<int>(cdiv(most, a.per));
+  a.N = qnf4::uu_cols(a.per, r8);
   a.n_alloc = lr_n_alloc(a.N);
   a.timeout_ns = g_timeout_ns.load();
-  const int64_t tiles = cdiv(M, 128), stages = cdiv(in, 64);
   // split K while the clusters of one group per token tile fit the SMs and
   // every CTA keeps two stages
   int ks = 1;
@@ -1028,6 +1038,61 @@ int launch_slots_us(const uint16_t* x, const uint16_t* A, const float* scale, co
   return QLORA_OK;
 }
 
+// The transposed GEMM for at most kSlotsFewTokens tokens.  ids null: every token
+// has adapter 0.  overlap: it may start while the kernel before it in the
+// stream runs; it waits for that kernel before it reads us or the tickets.
+int launch_slots_gemm(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, const uint16_t* B, int64_t n_adapters,
+                      int r, const uint16_t* us, const int32_t* ids, uint16_t* h, float* part, uint32_t* tickets,
+                      bool overlap, cudaStream_t st) {
+  const int64_t in = w->cols, out = w->rows;
+  qnf4::SlotsGemmArgs a{};
+  a.q8 = w->q8;
+  a.step2 = w->step2;
+  a.mean = w->mean;
+  a.us = us;
+  a.B = B;
+  a.ids = ids;
+  a.h = h;
+  a.part = part;
+  a.tickets = tickets;
+  a.n_adapters = n_adapters;
+  a.M = static_cast<int>(M);
+  a.out = static_cast<int>(out);
+  a.K = static_cast<int>(in);
+  a.r = r;
+  a.r8 = padded_rank(r);
+  a.N = static_cast<int>(cdiv(M, 16) * 16);
+  a.L = tables().L;
+  a.timeout_ns = g_timeout_ns.load();
+  CUtensorMap tm_codes, tm_x;
+  if (!make_tmap_codes(&tm_codes, w->codes, static_cast<uint64_t>(out), static_cast<uint64_t>(in / 2), qnf4::kSgRows) ||
+      !make_tmap_bf16_blocks(&tm_x, x, static_cast<uint64_t>(M), static_cast<uint64_t>(in),
+                             static_cast<uint32_t>(a.N), static_cast<uint32_t>(qnf4::sg_kb(a.N))))
+    return QLORA_ERR_CUDA;
+  const auto kern = a.N <= 32    ? qnf4::slots_gemm_kernel<4, 4, true>
+                    : a.N <= 64  ? qnf4::slots_gemm_kernel<4, 2, true>
+                    : a.N <= 128 ? qnf4::slots_gemm_kernel<2, 2, true>
+                                 : qnf4::slots_gemm_kernel<2, 2, false>;
+  const int smem = qnf4::sg_smem_bytes(a.N);
+  QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), smem));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(slots_ctas(in, out)));
+  cfg.blockDim = dim3(qnf4::kSgThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap && !g_timing_on.load() ? 1 : 0;   // (timed launches one after another)
+  {
+    LaunchTimer lt_("slots_gemm", st);
+    QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, tm_codes, tm_x, a));
+  }
+  QLORA_CUDA_TRY(cudaGetLastError());
+  return QLORA_OK;
+}
+
 int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, const uint16_t* A,
                           const uint16_t* B, int64_t n_adapters, int r, const float* scale, const int32_t* ids,
                           uint16_t* h, void* workspace, cudaStream_t st) {
@@ -1056,53 +1121,237 @@ int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* 
     QLORA_CUDA_TRY(cudaGetLastError());
     return QLORA_OK;
   }
-  qnf4::SlotsGemmArgs a{};
-  a.q8 = w->q8;
-  a.step2 = w->step2;
-  a.mean = w->mean;
-  a.us = us;
-  a.B = B;
-  a.ids = ids;
-  a.h = h;
-  a.part = reinterpret_cast<float*>(base + ws.part_off);
-  a.tickets = tickets;
-  a.n_adapters = n_adapters;
-  a.M = static_cast<int>(M);
-  a.out = static_cast<int>(out);
-  a.K = static_cast<int>(in);
+  return launch_slots_gemm(x, M, w, B, n_adapters, r, us, ids, h, reinterpret_cast<float*>(base + ws.part_off), tickets,
+                           true, st);
+}
+
+// ------------------------------------------------------------------ counter-based LoRA dropout
+qnf4::DropoutRng dropout_rng(const uint64_t* state, double p) {
+  return qnf4::DropoutRng{state, static_cast<uint32_t>(std::min(65535.0, std::nearbyint(p * 65536.0)))};
+}
+
+// The share kept with the rounded probability.
+float kept_share(const qnf4::DropoutRng& rng) { return 1.f - static_cast<float>(rng.threshold) / 65536.f; }
+
+// Tensor-memory columns of an rng rank-r launch: the SM's 512 shared by the
+// CTAs that its shared memory holds at once (a CTA that waited for another's
+// columns while both wait for their clusters could not finish).
+int lr_rng_alloc(int N, bool b_mn_major, int ring) {
+  const int resident = 228 * 1024 / (qnf4::lr_smem_bytes(N, b_mn_major, ring) + 1024);
+  return resident <= 1 ? 512 : resident == 2 ? 256 : 128;
+}
+
+// us = bf16(s (x k) A^T) with the mask drawn.
+int launch_us_rng(const uint16_t* x, const uint16_t* A, uint16_t* us, int64_t M, int64_t in, int r, float s,
+                  const qnf4::DropoutRng& rng, cudaStream_t st) {
+  qnf4::LrArgs a{};
   a.r = r;
-  a.r8 = r8;
-  a.N = static_cast<int>(cdiv(M, 16) * 16);
-  a.L = tables().L;
+  a.N = (r + 15) / 16 * 16;
+  a.K = static_cast<int>(in);
+  a.rng = rng;
+  const int tiles = static_cast<int>(cdiv(M, 128));
+  a.p[0] = qnf4::LrProblem{us, static_cast<int>(M), tiles, 0, s, nullptr, static_cast<int>(in), 1, a.N, 1, 1, r};
+  a.p[1] = a.p[0];
   a.timeout_ns = g_timeout_ns.load();
-  CUtensorMap tm_codes, tm_x;
-  if (!make_tmap_codes(&tm_codes, w->codes, static_cast<uint64_t>(out), static_cast<uint64_t>(in / 2), qnf4::kSgRows) ||
-      !make_tmap_bf16_blocks(&tm_x, x, static_cast<uint64_t>(M), static_cast<uint64_t>(in),
-                             static_cast<uint32_t>(a.N), static_cast<uint32_t>(qnf4::sg_kb(a.N))))
+  const int64_t stages = cdiv(in, 64);
+  const LrShape sh = lr_shape(tiles, stages, a.N, false);
+  const int ks = std::min(sh.ks, 4);           // as with a stored mask (launch_lora_row)
+  a.ring = sh.ring;
+  a.n_alloc = lr_rng_alloc(a.N, false, a.ring);
+  a.stages_per_split = static_cast<int>(cdiv(stages, ks));
+  CUtensorMap tm[4];
+  if (!make_tmap_bf16(&tm[0], x, M, in, 128) || !make_tmap_bf16(&tm[1], A, r, in, a.N)) return QLORA_ERR_CUDA;
+  tm[2] = tm[0];
+  tm[3] = tm[1];
+  return launch_lora_umma<false, false, true>(tm, a, ks, static_cast<unsigned>(tiles), "lora_rowwise", st);
+}
+
+// du = s dh B in three bf16 parts, [M, lr_part_cols(r)].
+int launch_du_parts(const uint16_t* dh, const uint16_t* B, uint16_t* du, int64_t M, int64_t out, int r, float s,
+                    cudaStream_t st) {
+  qnf4::LrArgs a{};
+  a.r = r;
+  a.N = (r + 15) / 16 * 16;
+  a.K = static_cast<int>(out);
+  const int tiles = static_cast<int>(cdiv(M, 128));
+  a.p[0] = qnf4::LrProblem{du, static_cast<int>(M), tiles, 0, s, nullptr, static_cast<int>(out), 0, a.N, 3, 1, r};
+  a.p[1] = a.p[0];
+  a.timeout_ns = g_timeout_ns.load();
+  const int64_t stages = cdiv(out, 64);
+  const LrShape sh = lr_shape(tiles, stages, a.N, true);
+  a.ring = sh.ring;
+  a.n_alloc = lr_rng_alloc(a.N, true, a.ring);
+  a.stages_per_split = static_cast<int>(cdiv(stages, sh.ks));
+  CUtensorMap tm[4];
+  if (!make_tmap_bf16(&tm[0], dh, M, out, 128) || !make_tmap_bf16(&tm[1], B, out, r, 64)) return QLORA_ERR_CUDA;
+  tm[2] = tm[0];
+  tm[3] = tm[1];
+  return launch_lora_umma<false, true, true>(tm, a, sh.ks, static_cast<unsigned>(tiles), "lora_rowwise_du", st);
+}
+
+// dB = dh^T us -> [out, r] and dA = du^T (x k) * dA_scale -> [r, in] in one launch, du in parts.
+int launch_grads_rng(const uint16_t* dh, const uint16_t* us, const uint16_t* x, const uint16_t* du, int64_t M,
+                     int64_t in, int64_t out, int r, float* dB, float* dA, float dA_scale,
+                     const qnf4::DropoutRng& rng, cudaStream_t st) {
+  qnf4::LrArgs a{};
+  const int gr = qnf4::lr_group_ranks(r), groups = qnf4::lr_groups(r), cols = qnf4::lr_part_cols(r);
+  const int n_dB = (r + 15) / 16 * 16, n_dA = (3 * gr + 15) / 16 * 16;
+  a.r = r;
+  a.N = std::max(n_dB, n_dA);
+  a.K = static_cast<int>(M);
+  a.rng = rng;
+  const int t_dB = static_cast<int>(cdiv(out, 128)), t_dA = static_cast<int>(cdiv(in, 128)) * groups;
+  a.p[0] = qnf4::LrProblem{dB, static_cast<int>(out), t_dB, 0, 1.f, nullptr, static_cast<int>(out), 0, n_dB, 1, 1, r};
+  a.p[1] = qnf4::LrProblem{dA, static_cast<int>(in), t_dA, 1, dA_scale, nullptr, static_cast<int>(in), 1,
+                           n_dA, 3, groups, gr};
+  a.timeout_ns = g_timeout_ns.load();
+  const int64_t stages = cdiv(M, 64);
+  const LrShape sh = lr_shape(t_dB + t_dA, stages, a.N, true);
+  int ks = sh.ks;
+  a.ring = sh.ring;
+  a.n_alloc = lr_rng_alloc(a.N, true, a.ring);
+  // at most 32 stages (128 steps of the tensor cores' sum) per CTA and accumulator
+  const int n_acc = std::max(1, std::min(8, a.n_alloc / ((a.N + 31) / 32 * 32)));
+  while (ks < 8 && cdiv(stages, ks) > 32 * n_acc) ks *= 2;
+  a.stages_per_split = static_cast<int>(cdiv(stages, ks));
+  CUtensorMap tm[4];
+  if (!make_tmap_bf16(&tm[0], dh, M, out, 64) || !make_tmap_bf16(&tm[1], us, M, r, 64) ||
+      !make_tmap_bf16(&tm[2], x, M, in, 64) || !make_tmap_bf16(&tm[3], du, M, cols, 64))
     return QLORA_ERR_CUDA;
-  const auto kern = a.N <= 32    ? qnf4::slots_gemm_kernel<4, 4, true>
-                    : a.N <= 64  ? qnf4::slots_gemm_kernel<4, 2, true>
-                    : a.N <= 128 ? qnf4::slots_gemm_kernel<2, 2, true>
-                                 : qnf4::slots_gemm_kernel<2, 2, false>;
-  const int smem = qnf4::sg_smem_bytes(a.N);
-  QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), smem));
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(slots_ctas(in, out)));
-  cfg.blockDim = dim3(qnf4::kSgThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  // may start while the rank-r kernel runs; it waits for it before it reads us or the tickets
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = g_timing_on.load() ? 0 : 1;               // (timed launches one after another)
-  {
-    LaunchTimer lt_("slots_gemm", st);
-    QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, tm_codes, tm_x, a));
+  return launch_lora_umma<true, true, true>(tm, a, ks, static_cast<unsigned>(t_dB + t_dA), "lora_colwise", st);
+}
+
+// Forward workspace: for few tokens those of the transposed GEMM, then the
+// few-token rank-r partials and ticket; then the padded copies (r % 8 != 0).
+size_t fwd_rng_base_ws(int64_t M, int64_t in, int64_t out, int r) {
+  return M <= kSlotsFewTokens ? slots_ws(M, in, out, r).total + fewtok_ws(in, r) : 0;
+}
+
+size_t fwd_rng_ws(int64_t M, int64_t in, int64_t out, int r) {
+  return pad_ws(M, in, out, r, false, fwd_rng_base_ws(M, in, out, r)).total;
+}
+
+BwdWs bwd_rng_ws(int64_t M, int64_t in, int64_t out, int r) {
+  BwdWs w{};
+  w.pad = pad_ws(M, in, out, r, true, round256(static_cast<size_t>(M) * qnf4::lr_part_cols(padded_rank(r)) * 2));
+  w.total = w.pad.total;
+  return w;
+}
+
+// Forward after validation, rank a multiple of 8.
+int linear_fwd_rng_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, const uint16_t* A,
+                        const uint16_t* B, int r, float s_lora, const qnf4::DropoutRng& rng, uint16_t* h,
+                        uint16_t* us, void* workspace, cudaStream_t st) {
+  const int64_t in = w->cols, out = w->rows;
+  if (M > 16) {
+    const int rc = launch_us_rng(x, A, us, M, in, r, s_lora, rng, st);
+    if (rc != QLORA_OK) return rc;
+  } else {
+    uint8_t* ft = static_cast<uint8_t*>(workspace) + slots_ws(M, in, out, r).total;
+    float* part = reinterpret_cast<float*>(ft);
+    unsigned int* ticket = reinterpret_cast<unsigned int*>(ft + fewtok_ws(in, r) - 256);
+    QLORA_CUDA_TRY(cudaMemsetAsync(ticket, 0, sizeof(unsigned int), st));
+    const unsigned chunks = static_cast<unsigned>(cdiv(in, qnf4::kFtChunk));
+    {
+      LaunchTimer lt_("lora_fewtok", st);
+      if (M > 8)
+        qnf4::fewtok_us_kernel<16, true><<<chunks, qnf4::kFtThreads, 0, st>>>(x, nullptr, A, static_cast<int>(M), in, r,
+                                                                           s_lora, part, ticket, us, rng);
+      else
+        qnf4::fewtok_us_kernel<8, true><<<chunks, qnf4::kFtThreads, 0, st>>>(x, nullptr, A, static_cast<int>(M), in, r,
+                                                                          s_lora, part, ticket, us, rng);
+    }
+    QLORA_CUDA_TRY(cudaGetLastError());
   }
-  QLORA_CUDA_TRY(cudaGetLastError());
-  return QLORA_OK;
+  if (M > kSlotsFewTokens) return launch_gemm(false, w, x, M, in, us, B, r, h, out, st);   // h = [x|us] [W0|B]^T
+  const SlotsWs sw = slots_ws(M, in, out, r);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  uint32_t* tickets = reinterpret_cast<uint32_t*>(base + sw.ticket_off);
+  QLORA_CUDA_TRY(cudaMemsetAsync(tickets, 0, static_cast<size_t>(cdiv(out, qnf4::kSgRows)) * 4, st));
+  return launch_slots_gemm(x, M, w, B, 1, r, us, nullptr, h, reinterpret_cast<float*>(base + sw.part_off), tickets,
+                           false, st);
+}
+
+int linear_fwd_rng_any_rank(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, const uint16_t* A,
+                            const uint16_t* B, int r, float s_lora, const qnf4::DropoutRng& rng, uint16_t* h,
+                            uint16_t* us_out, void* workspace, cudaStream_t st) {
+  if (r % 8 == 0) return linear_fwd_rng_impl(x, M, w, A, B, r, s_lora, rng, h, us_out, workspace, st);
+  const int64_t in = w->cols, out = w->rows;
+  const int rp = padded_rank(r);
+  const PadWs pw = pad_ws(M, in, out, r, false, fwd_rng_base_ws(M, in, out, r));
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  uint16_t* A_p = reinterpret_cast<uint16_t*>(base + pw.a_off);
+  uint16_t* B_p = reinterpret_cast<uint16_t*>(base + pw.b_off);
+  uint16_t* us_p = reinterpret_cast<uint16_t*>(base + pw.us_off);
+  int rc = launch_copy_pad(A, r, in, A_p, rp, in, st);
+  if (rc == QLORA_OK) rc = launch_copy_pad(B, out, r, B_p, out, rp, st);
+  if (rc == QLORA_OK) rc = linear_fwd_rng_impl(x, M, w, A_p, B_p, rp, s_lora, rng, h, us_p, workspace, st);
+  if (rc == QLORA_OK) rc = launch_copy_pad(us_p, M, rp, us_out, M, r, st);
+  return rc;
+}
+
+// Backward after validation, rank a multiple of 8; the streams as in
+// linear_bwd_impl with a mask.
+int linear_bwd_rng_impl(const uint16_t* dh, const uint16_t* x, const uint16_t* us, int64_t M,
+                        const qlora_nf4_weight* w, const uint16_t* A, const uint16_t* B, int r, float s,
+                        const qnf4::DropoutRng& rng, uint16_t* dx, float* dA, float* dB, uint16_t* du,
+                        cudaStream_t st) {
+  const int64_t in = w->cols, out = w->rows;
+  const float inv_keep = 1.f / kept_share(rng);
+  GroupStreams& g = group_streams();
+  std::lock_guard<std::mutex> lock(g.mu);
+  const int rc0 = ensure_group_streams(g, 4);
+  if (rc0 != QLORA_OK) return rc0;
+  QLORA_CUDA_TRY(cudaEventRecord(g.ev[0], st));
+  QLORA_CUDA_TRY(cudaStreamWaitEvent(g.hi, g.ev[0], 0));
+  QLORA_CUDA_TRY(cudaStreamWaitEvent(g.lo, g.ev[0], 0));
+  int rc = launch_gemm(true, w, dh, M, out, nullptr, nullptr, 0, dx, in, g.hi);          // dx = dh W0
+  if (rc == QLORA_OK) rc = launch_du_parts(dh, B, du, M, out, r, s, g.lo);              // du = s dh B
+  if (rc == QLORA_OK && cudaEventRecord(g.ev[1], g.lo) != cudaSuccess) rc = QLORA_ERR_CUDA;
+  if (rc == QLORA_OK) rc = launch_grads_rng(dh, us, x, du, M, in, out, r, dB, dA, inv_keep, rng, g.lo);
+  if (rc == QLORA_OK && cudaStreamWaitEvent(g.hi, g.ev[1], 0) != cudaSuccess) rc = QLORA_ERR_CUDA;
+  if (rc == QLORA_OK) {
+    const int64_t tiles = cdiv(M, qnf4::kDxTileRows) * cdiv(in, qnf4::kDxTileCols);
+    const int smem = qnf4::dx_smem_bytes(r);
+    if (set_max_smem(reinterpret_cast<const void*>(qnf4::dropout_dx_kernel<true>), smem) != cudaSuccess) {
+      rc = QLORA_ERR_CUDA;
+    } else {
+      LaunchTimer lt_("dropout_dx", g.hi);
+      qnf4::dropout_dx_kernel<true><<<static_cast<unsigned>(tiles), qnf4::kDxThreads, smem, g.hi>>>(
+          dx, du, A, nullptr, M, in, r, inv_keep, rng);                                   // + (du A) k/(1-p)
+      if (cudaGetLastError() != cudaSuccess) rc = QLORA_ERR_CUDA;
+    }
+  }
+  // join both streams back into `st` (after an error too)
+  QLORA_CUDA_TRY(cudaEventRecord(g.ev[2], g.hi));
+  QLORA_CUDA_TRY(cudaEventRecord(g.ev[3], g.lo));
+  QLORA_CUDA_TRY(cudaStreamWaitEvent(st, g.ev[2], 0));
+  QLORA_CUDA_TRY(cudaStreamWaitEvent(st, g.ev[3], 0));
+  return rc;
+}
+
+int linear_bwd_rng_any_rank(const uint16_t* dh, const uint16_t* x, const uint16_t* us, int64_t M,
+                            const qlora_nf4_weight* w, const uint16_t* A, const uint16_t* B, int r, float s,
+                            const qnf4::DropoutRng& rng, uint16_t* dx, float* dA, float* dB, void* workspace,
+                            cudaStream_t st) {
+  const int64_t in = w->cols, out = w->rows;
+  const BwdWs ws = bwd_rng_ws(M, in, out, r);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  uint16_t* du = reinterpret_cast<uint16_t*>(base + ws.du_off);
+  if (r % 8 == 0) return linear_bwd_rng_impl(dh, x, us, M, w, A, B, r, s, rng, dx, dA, dB, du, st);
+  const int rp = padded_rank(r);
+  uint16_t* A_p = reinterpret_cast<uint16_t*>(base + ws.pad.a_off);
+  uint16_t* B_p = reinterpret_cast<uint16_t*>(base + ws.pad.b_off);
+  uint16_t* us_p = reinterpret_cast<uint16_t*>(base + ws.pad.us_off);
+  float* dA_p = reinterpret_cast<float*>(base + ws.pad.da_off);
+  float* dB_p = reinterpret_cast<float*>(base + ws.pad.db_off);
+  int rc = launch_copy_pad(A, r, in, A_p, rp, in, st);
+  if (rc == QLORA_OK) rc = launch_copy_pad(B, out, r, B_p, out, rp, st);
+  if (rc == QLORA_OK) rc = launch_copy_pad(us, M, r, us_p, M, rp, st);
+  if (rc == QLORA_OK) rc = linear_bwd_rng_impl(dh, x, us_p, M, w, A_p, B_p, rp, s, rng, dx, dA_p, dB_p, du, st);
+  if (rc == QLORA_OK) rc = launch_copy_pad(dA_p, rp, in, dA, r, in, st);
+  if (rc == QLORA_OK) rc = launch_copy_pad(dB_p, out, rp, dB, out, r, st);
+  return rc;
 }
 
 // The rank-r work of a projection moves to the low-priority stream only on
@@ -1169,6 +1418,12 @@ size_t qlora_workspace_size(int op, int64_t M, int64_t in_features, int64_t out_
     case QLORA_OP_LINEAR_BWD_DROPOUT:
       if (M < 1 || r < 1) return 0;
       return bwd_ws(M, in_features, out_features, r).total;
+    case QLORA_OP_LINEAR_FWD_DROPOUT_RNG:
+      if (M < 1 || r < 1 || in_features < 64 || out_features < 64) return 0;
+      return fwd_rng_ws(M, in_features, out_features, r);
+    case QLORA_OP_LINEAR_BWD_DROPOUT_RNG:
+      if (M < 1 || r < 1) return 0;
+      return bwd_rng_ws(M, in_features, out_features, r).total;
     case QLORA_OP_LINEAR_FWD_SLOTS:
       if (M < 1 || r < 1 || in_features < 64 || out_features < 64) return 0;
       return slots_ws(M, in_features, out_features, r).total;
@@ -1531,6 +1786,49 @@ int qlora_linear_fwd_slots(const uint16_t* x, int64_t M, const qlora_nf4_weight*
     return QLORA_ERR_WORKSPACE;
   return linear_fwd_slots_impl(x, M, w, A, B, n_adapters, r, scale, ids, h, workspace,
                                static_cast<cudaStream_t>(stream));
+}
+
+int qlora_dropout_keep_bits(const uint64_t* rng, double p, int64_t M, int64_t n, uint8_t* keep_bits, void* stream) {
+  if (!rng || !aligned(rng, 8) || !(p >= 0.0 && p < 1.0) || M < 0) return QLORA_ERR_INVALID_ARG;
+  if (M > 0 && (!keep_bits || !aligned(keep_bits, 4))) return QLORA_ERR_INVALID_ARG;
+  if (n < 64 || n % 64 != 0 || n > (1ll << 30) || M > kMaxTokens) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return QLORA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  {
+    LaunchTimer lt_("keep_bits", st);
+    const dim3 grid(static_cast<unsigned>(cdiv(n / 32, 256)), static_cast<unsigned>(std::min<int64_t>(M, 65535)));
+    qnf4::keep_bits_kernel<<<grid, 256, 0, st>>>(dropout_rng(rng, p), M, n, reinterpret_cast<uint32_t*>(keep_bits));
+  }
+  QLORA_CUDA_TRY(cudaGetLastError());
+  return QLORA_OK;
+}
+
+int qlora_linear_fwd_dropout_rng(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, const uint16_t* A,
+                                 const uint16_t* B, int r, float alpha, const uint64_t* rng, double p, uint16_t* h,
+                                 uint16_t* us_out, void* workspace, size_t workspace_bytes, void* stream) {
+  const int sc = check_fwd_args(x, M, w, A, B, r, alpha, h, us_out);
+  if (sc != QLORA_OK) return sc;
+  if (!rng || !aligned(rng, 8) || !(p >= 0.0 && p < 1.0)) return QLORA_ERR_INVALID_ARG;
+  const size_t need = fwd_rng_ws(M, w->cols, w->rows, r);
+  if (need > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need))
+    return QLORA_ERR_WORKSPACE;
+  const qnf4::DropoutRng d = dropout_rng(rng, p);
+  return linear_fwd_rng_any_rank(x, M, w, A, B, r, (alpha / static_cast<float>(r)) / kept_share(d), d, h, us_out,
+                                 workspace, static_cast<cudaStream_t>(stream));
+}
+
+int qlora_linear_bwd_dropout_rng(const uint16_t* dh, const uint16_t* x, const uint16_t* us, int64_t M,
+                                 const qlora_nf4_weight* w, const uint16_t* A, const uint16_t* B, int r, float alpha,
+                                 const uint64_t* rng, double p, uint16_t* dx, float* dA, float* dB, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const int sc = check_bwd_args(dh, x, us, M, w, A, B, r, alpha, dx, dA, dB);
+  if (sc != QLORA_OK) return sc;
+  if (!rng || !aligned(rng, 8) || !(p >= 0.0 && p < 1.0)) return QLORA_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < bwd_rng_ws(M, w->cols, w->rows, r).total)
+    return QLORA_ERR_WORKSPACE;
+  return linear_bwd_rng_any_rank(dh, x, us, M, w, A, B, r, alpha / static_cast<float>(r), dropout_rng(rng, p), dx, dA,
+                                 dB, workspace, static_cast<cudaStream_t>(stream));
 }
 
 int qlora_last_device_status(void* stream) {

@@ -13,6 +13,8 @@
 #pragma once
 
 #include "common.cuh"
+#include "lora_sm100.cuh"
+#include "philox.cuh"
 
 namespace qnf4 {
 
@@ -39,9 +41,13 @@ __host__ __device__ constexpr int dx_smem_bytes(int r) {
   return stage > p ? stage : p;
 }
 
+// kRng: the keep bits are drawn (philox.cuh), and du is given in parts
+// (lora_sm100.cuh), of which the first, its bf16 value, is used: dx is rounded
+// to bf16 anyway.
+template <bool kRng>
 __global__ void __launch_bounds__(kDxThreads) dropout_dx_kernel(
     uint16_t* __restrict__ dx, const uint16_t* __restrict__ du, const uint16_t* __restrict__ A,
-    const uint8_t* __restrict__ keep_bits, int64_t M, int64_t n, int r, float inv_keep) {
+    const uint8_t* __restrict__ keep_bits, int64_t M, int64_t n, int r, float inv_keep, DropoutRng rng) {
   extern __shared__ __align__(16) uint8_t s_dx[];
   const int rk = dx_rank_pad(r);
   const int du_pitch = dx_du_pitch(r);
@@ -56,7 +62,10 @@ __global__ void __launch_bounds__(kDxThreads) dropout_dx_kernel(
   for (int e = threadIdx.x; e < kDxTileRows * (rk / 8); e += kDxThreads) {
     const int row = e / (rk / 8), ch = e % (rk / 8);
     const bool ok = m0 + row < M && ch * 8 < r;
-    cp_async_16(smem_u32(s_du + row * du_pitch + ch * 16), du + (ok ? (m0 + row) * r + ch * 8 : 0), ok);
+    const int64_t at = kRng ? (m0 + row) * lr_part_cols(r) + ch * 8 / lr_group_ranks(r) * 3 * lr_group_ranks(r) +
+                                  ch * 8 % lr_group_ranks(r)
+                            : (m0 + row) * r + ch * 8;
+    cp_async_16(smem_u32(s_du + row * du_pitch + ch * 16), du + (ok ? at : 0), ok);
   }
   for (int e = threadIdx.x; e < rk * (kDxTileCols / 8); e += kDxThreads) {
     const int row = e / (kDxTileCols / 8), ch = e % (kDxTileCols / 8);
@@ -110,6 +119,8 @@ __global__ void __launch_bounds__(kDxThreads) dropout_dx_kernel(
   // dx += (k / (1 - p)) * P, 8 columns of one row per thread and unit; all
   // of a thread's dx and keep loads are issued before any store
   constexpr int kUnits = kDxTileRows * (kDxTileCols / 8) / kDxThreads;   // 8
+  PhiloxKey key{};
+  if (kRng) key = philox_key(rng.state);
   uint4 dv[kUnits];
   uint32_t kv[kUnits];
 #pragma unroll
@@ -121,7 +132,8 @@ __global__ void __launch_bounds__(kDxThreads) dropout_dx_kernel(
     kv[u] = 0;
     if (m < M && i < n) {
       dv[u] = *reinterpret_cast<const uint4*>(dx + m * n + i);
-      kv[u] = __ldg(keep_bits + m * (n / 8) + i / 8);
+      kv[u] = kRng ? philox_keep8(key, rng.threshold, static_cast<uint32_t>(m), static_cast<uint32_t>(i / 8))
+                   : __ldg(keep_bits + m * (n / 8) + i / 8);
     }
   }
 #pragma unroll

@@ -12,6 +12,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "philox.cuh"
 
 namespace qnf4 {
 
@@ -28,11 +29,12 @@ __device__ __forceinline__ float fewtok_bf16_lo(uint32_t w) { return __uint_as_f
 __device__ __forceinline__ float fewtok_bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // kTok: token rows processed (8 or 16, >= M).  r % 8 == 0, K % 64 == 0.
-template <int kTok>
+// kRng: the keep bits are drawn (philox.cuh) instead of read.
+template <int kTok, bool kRng = false>
 __global__ void __launch_bounds__(kFtThreads) fewtok_us_kernel(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ keep, const uint16_t* __restrict__ A, int M,
     int64_t K, int r, float s, float* __restrict__ part, unsigned int* __restrict__ ticket,
-    uint16_t* __restrict__ us) {
+    uint16_t* __restrict__ us, DropoutRng rng) {
   __shared__ __align__(16) float xs[kTok][kFtChunk];
   __shared__ bool is_last;
   const int c = blockIdx.x;
@@ -46,8 +48,10 @@ __global__ void __launch_bounds__(kFtThreads) fewtok_us_kernel(
     uint4 v = make_uint4(0, 0, 0, 0);
     if (m < M && 8 * c8 < kc) {
       v = __ldg(reinterpret_cast<const uint4*>(x + m * K + k0 + 8 * c8));
-      if (keep != nullptr) {
-        const uint32_t kb = __ldg(keep + m * (K / 8) + k0 / 8 + c8);
+      if (kRng || keep != nullptr) {
+        const uint32_t kb = kRng ? philox_keep8(philox_key(rng.state), rng.threshold, static_cast<uint32_t>(m),
+                                                static_cast<uint32_t>(k0 / 8 + c8))
+                                 : __ldg(keep + m * (K / 8) + k0 / 8 + c8);
         v.x &= ((kb & 1u) ? 0x0000FFFFu : 0u) | ((kb & 2u) ? 0xFFFF0000u : 0u);
         v.y &= ((kb & 4u) ? 0x0000FFFFu : 0u) | ((kb & 8u) ? 0xFFFF0000u : 0u);
         v.z &= ((kb & 16u) ? 0x0000FFFFu : 0u) | ((kb & 32u) ? 0xFFFF0000u : 0u);

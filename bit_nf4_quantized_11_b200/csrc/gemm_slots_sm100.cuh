@@ -94,7 +94,7 @@ struct SlotsGemmArgs {
   const float* mean;
   const uint16_t* us;       // [M, r8]
   const uint16_t* B;        // [n_adapters, out, r]
-  const int32_t* ids;       // [M]
+  const int32_t* ids;       // [M], or null: adapter 0 throughout
   uint16_t* h;              // [M, out]
   float* part;              // [2 * CTAs][N][128]: a CTA's first and last tile, where cut
   uint32_t* tickets;        // [row tiles], zero before the launch
@@ -254,7 +254,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   // ones; the hash table lies over the code ring, which is not in use yet.
   int32_t my_id = -1;
   if (threadIdx.x < kSgMaxN && static_cast<int>(threadIdx.x) < args.M) {
-    my_id = __ldg(args.ids + threadIdx.x);
+    my_id = args.ids != nullptr ? __ldg(args.ids + threadIdx.x) : 0;
     if (my_id < 0 || my_id >= args.n_adapters) my_id = -1;
   }
   if (kLut) {

@@ -33,9 +33,22 @@
 // Every wait is bounded: on timeout the CTA sets the device error flag,
 // issues nothing more, waits (bounded) for what it issued and exits.
 // No TMA multicast is used.
+//
+// kRng: the same products for counter-based LoRA dropout (philox.cuh).
+//   * The masking warps draw the keep bits of the staged tile instead of
+//     loading them.
+//   * dA is a sum over tokens of du x, so du rounded to bf16 would leave a
+//     relative error of 2^-9 in the fp32 gradient.  du is kept as three bf16
+//     parts whose sum is its fp32 value (hi, mid, lo columns side by side, at
+//     most 80 ranks per column group so that 3 x 80 <= 256), dA multiplies by
+//     all three and adds the three results.
+//   * The tensor cores cut the fp32 sum at every step, always towards zero:
+//     after 256 steps of 16 tokens the error was 4e-6.  The stages take turns
+//     over several accumulators, which the epilogue adds up.
 #pragma once
 
 #include "common.cuh"
+#include "philox.cuh"
 
 namespace qnf4 {
 
@@ -60,6 +73,12 @@ struct LrProblem {
   float scale;
   const uint8_t* keep;   // LoRA dropout keep bits of the token operand [tokens, features / 8], or null
   int features;          // columns of the token operand (row form: K; col form: rows)
+  // kRng only:
+  int masked;            // draw the keep bits
+  int N;                 // columns of the product
+  int parts;             // row form: bf16 parts written per value; col form: column sets added up
+  int groups;            // col form: column groups (tiles of group g follow those of g - 1)
+  int group_ranks;       // ranks per column group
 };
 
 struct LrArgs {
@@ -71,7 +90,15 @@ struct LrArgs {
   int stages_per_split;  // 64-wide contraction stages per CTA of the cluster
   int ring;              // shared-memory stages in flight (<= kLrMaxStages)
   uint64_t timeout_ns;
+  DropoutRng rng;        // kRng only
 };
+
+// du as parts: rank j of a row lies at (j / kLrPartRanks) 3 kLrPartRanks + part * ranks-of-its-group + ...
+constexpr int kLrPartRanks = 80;
+// Ranks per column group and columns of a row of du in parts, for a rank r (r % 8 == 0).
+__host__ __device__ constexpr int lr_group_ranks(int r) { return r <= kLrPartRanks ? r : kLrPartRanks; }
+__host__ __device__ constexpr int lr_groups(int r) { return (r + lr_group_ranks(r) - 1) / lr_group_ranks(r); }
+__host__ __device__ constexpr int lr_part_cols(int r) { return lr_groups(r) * 3 * lr_group_ranks(r); }
 
 // Shared bytes of one stage of the B operand (N rows x 64 k K-major, or
 // ceil(N / 64) atoms of 64 n x 64 k) and of the fp32 partial tile (padded rows).
@@ -87,7 +114,7 @@ __host__ __device__ constexpr int lr_smem_bytes(int N, bool b_mn_major, int stag
 
 // kCol: col form (A MN-major, output fp32); otherwise row form (A K-major,
 // output bf16).  kBMN: B operand N-major.
-template <bool kCol, bool kBMN>
+template <bool kCol, bool kBMN, bool kRng = false>
 __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
     const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1, const LrArgs args) {
@@ -118,8 +145,19 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
   const float p_scale = prob == 0 ? args.p[0].scale : args.p[1].scale;
   const uint8_t* const p_keep = prob == 0 ? args.p[0].keep : args.p[1].keep;
   const int p_features = prob == 0 ? args.p[0].features : args.p[1].features;
-  const bool do_mask = p_keep != nullptr;                            // CTA-uniform
-  const int tile = prob == 0 ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) - args.p[0].tiles;
+  const bool do_mask = kRng ? (prob == 0 ? args.p[0].masked : args.p[1].masked) != 0
+                            : p_keep != nullptr;                     // CTA-uniform
+  const int p_tile = prob == 0 ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) - args.p[0].tiles;
+  // (kRng) this CTA's columns: width, first column, bf16 parts
+  const int p_N = kRng ? (prob == 0 ? args.p[0].N : args.p[1].N) : N;
+  const int p_parts = kRng ? (prob == 0 ? args.p[0].parts : args.p[1].parts) : 1;
+  const int p_ranks = kRng ? (prob == 0 ? args.p[0].group_ranks : args.p[1].group_ranks) : args.r;
+  const int p_row_tiles = (p_rows + kLrTileRows - 1) / kLrTileRows;
+  const int p_group = kRng && kCol ? p_tile / p_row_tiles : 0;
+  const int tile = kRng && kCol ? p_tile % p_row_tiles : p_tile;
+  // accumulators that the stages take turns over
+  const int acc_stride = (p_N + 31) / 32 * 32;
+  const int n_acc = kRng ? max(1, min(8, args.n_alloc / acc_stride)) : 1;
   const CUtensorMap* tm_a = prob == 0 ? &tm_a0 : &tm_a1;
   const CUtensorMap* tm_b = prob == 0 ? &tm_b0 : &tm_b1;
   const int row0 = tile * kLrTileRows;
@@ -158,7 +196,7 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     }
   };
 
-  const uint32_t stage_tx = static_cast<uint32_t>(kLrAStage + b_stage);
+  const uint32_t stage_tx = static_cast<uint32_t>(kLrAStage + (kRng ? lr_b_stage(p_N, kBMN) : b_stage));
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -182,7 +220,8 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
         if (!kBMN) {
           tma_load_2d(b_dst, tm_b, full + s, k0, 0);                         // [N rows x 64 k]
         } else {
-          for (int a = 0; a * 64 < N; ++a) tma_load_2d(b_dst + a * 8192, tm_b, full + s, a * 64, k0);
+          const int c0 = kRng ? p_group * p_parts * p_ranks : 0;
+          for (int a = 0; a * 64 < p_N; ++a) tma_load_2d(b_dst + a * 8192, tm_b, full + s, c0 + a * 64, k0);
         }
         ++issued;
       }
@@ -193,7 +232,7 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
   } else if (warp == 1) {
     if (lane == 0) {
       // ------------------------------------------------------------ MMA issuer
-      const uint32_t idesc = umma_idesc_bf16_ab(kLrTileRows, N, kCol, kBMN);
+      const uint32_t idesc = umma_idesc_bf16_ab(kLrTileRows, p_N, kCol, kBMN);
       for (int it = 0; it < n_iter; ++it) {
         const int s = it % S;
         wait(full + s, (it / S) & 1u);
@@ -208,7 +247,10 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
                                       : umma_desc_sw128(a_base + kk * 32, 16, 1024);
           const uint64_t bdesc = kBMN ? umma_desc_sw128(b_base + kk * 2048, 8192, 1024)
                                       : umma_desc_sw128(b_base + kk * 32, 16, 1024);
-          umma_bf16_ss(tmem_base, adesc, bdesc, idesc, (it > 0 || kk > 0) ? 1u : 0u);
+          if (kRng)
+            umma_bf16_ss(tmem_base + (it % n_acc) * acc_stride, adesc, bdesc, idesc, (it >= n_acc || kk > 0) ? 1u : 0u);
+          else
+            umma_bf16_ss(tmem_base, adesc, bdesc, idesc, (it > 0 || kk > 0) ? 1u : 0u);
         }
         umma_commit(empty + s);
       }
@@ -264,20 +306,39 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
         if (src != nullptr) asm volatile("prefetch.global.L2 [%0];" :: "l"(src));
       }
     };
-    for (int i = 2; i < 6; ++i) prefetch_keep(i);
+    PhiloxKey key{};
+    if (kRng) key = philox_key(args.rng.state);
+    // the 32 keep bits of item h of stage `it`, drawn (past the tokens or
+    // features nothing reads them)
+    auto draw_keep = [&](int it, int h) -> uint32_t {
+      const int j = t + MT * h, i = j & (kLrTileRows - 1), q = j >> 7;
+      const int k0 = (st_begin + it) * 64;
+      const int tok = kCol ? k0 + (i & 63) : row0 + i;
+      const int f0 = kCol ? row0 + 64 * (i >> 6) : k0;
+      return philox_keep32(key, args.rng.threshold, static_cast<uint32_t>(tok), static_cast<uint32_t>(f0 / 8 + 4 * q));
+    };
+    if (!kRng)
+      for (int i = 2; i < 6; ++i) prefetch_keep(i);
     uint32_t kb_n1[4], kb_n2[4];
-    load_keep(0, kb_n1);
-    load_keep(1, kb_n2);
+    if (!kRng) {
+      load_keep(0, kb_n1);
+      load_keep(1, kb_n2);
+    }
     for (int it = 0; it < n_iter; ++it) {
       const int s = it % S;
       uint32_t kb[4];
+      if (kRng) {
+        kb[0] = draw_keep(it, 0);                                    // (256 masking threads: one item each)
+        kb[1] = kb[2] = kb[3] = 0;
+      } else {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        kb[h] = kb_n1[h];
-        kb_n1[h] = kb_n2[h];
+        for (int h = 0; h < 4; ++h) {
+          kb[h] = kb_n1[h];
+          kb_n1[h] = kb_n2[h];
+        }
+        load_keep(it + 2, kb_n2);
+        prefetch_keep(it + 6);
       }
-      load_keep(it + 2, kb_n2);
-      prefetch_keep(it + 6);
       wait(full + s, (it / S) & 1u);
       if (*abort_flag) break;
       const uint32_t a_base = smem_u32(a_ring + s * kLrAStage);
@@ -307,13 +368,22 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
   wait(acc_full, 0);
   tc_fence_after_sync();
   const int row = warp * 32 + lane;                                  // this thread's TMEM lane / tile row
-  const int pitch = lr_partial_pitch(N);
+  const int pitch = lr_partial_pitch(p_N);
   uint8_t* part = smem;                                              // the ring is free once acc_full completed
   __syncthreads();                                                   // every stage read by the tensor cores
-  for (int c0 = 0; warp < 4 && c0 < N; c0 += 32) {
+  for (int c0 = 0; warp < 4 && c0 < p_N; c0 += 32) {
     uint32_t v[32];
     tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + c0, v);
     tmem_ld_wait();
+    if (kRng) {
+      for (int g = 1; g < n_acc && g < n_iter; ++g) {
+        uint32_t w[32];
+        tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + g * acc_stride + c0, w);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+      }
+    }
     if (n_iter == 0) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0u;                        // nothing accumulated
@@ -321,7 +391,7 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     const uint32_t dst = smem_u32(part + row * pitch + c0 * 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c0 + 4 * i < N) sts_v4(dst + 16 * i, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      if (c0 + 4 * i < p_N) sts_v4(dst + 16 * i, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -330,7 +400,8 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
   // this CTA's share of the tile's rows, summed over the cluster in rank order
   const int share = kLrTileRows / ks;
   const int r_lo = split * share;
-  const int n4 = args.r / 4;                                         // float4 groups of the rank
+  // float4 groups of this CTA's ranks
+  const int n4 = (kRng ? min(p_ranks, args.r - p_group * p_ranks) : args.r) / 4;
   for (int e = threadIdx.x; e < share * n4; e += static_cast<int>(blockDim.x)) {
     int rr, c4;
     if (kCol && p_transpose) {                                   // rows fastest: coalesced dA^T stores
@@ -353,18 +424,51 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
                      : "=f"(u.x), "=f"(u.y), "=f"(u.z), "=f"(u.w) : "r"(mapa_shared(addr, rk)) : "memory");
       }
       t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+      if (kRng && kCol) {
+        for (int q = 1; q < p_parts; ++q) {                          // the parts of du: hi, then mid, then lo
+          const uint32_t addr_q = addr + q * p_ranks * 4;
+          if (ks == 1) {
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(u.x), "=f"(u.y), "=f"(u.z), "=f"(u.w)
+                         : "r"(addr_q) : "memory");
+          } else {
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(u.x), "=f"(u.y), "=f"(u.z), "=f"(u.w) : "r"(mapa_shared(addr_q, rk)) : "memory");
+          }
+          t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+        }
+      }
     }
     if (grow >= p_rows) continue;
     const float sc = p_scale;
-    if (!kCol) {
+    if (kRng && !kCol && p_parts == 3) {
+      // du in three bf16 parts, each the rounding of what the ones before leave
+      const int j = c4 * 4, gr = lr_group_ranks(args.r);
+      uint16_t* o = static_cast<uint16_t*>(p_out) + static_cast<int64_t>(grow) * lr_part_cols(args.r) +
+                    j / gr * 3 * gr + j % gr;                        // (gr % 8 == 0: four ranks of one group)
+      float f[4] = {t.x * sc, t.y * sc, t.z * sc, t.w * sc};
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i] = pack_bf16x2_rn(f[2 * i], f[2 * i + 1]);
+        *reinterpret_cast<uint2*>(o + q * gr) = make_uint2(w[0], w[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {                                // exact; 0 past an infinity or NaN
+          const float lo = f[2 * i] - __uint_as_float(w[i] << 16);
+          const float hi = f[2 * i + 1] - __uint_as_float(w[i] & 0xFFFF0000u);
+          f[2 * i] = isfinite(lo) ? lo : 0.f;
+          f[2 * i + 1] = isfinite(hi) ? hi : 0.f;
+        }
+      }
+    } else if (!kCol) {
       uint16_t* o = static_cast<uint16_t*>(p_out) + static_cast<int64_t>(grow) * args.r + c4 * 4;
       *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2_rn(t.x * sc, t.y * sc), pack_bf16x2_rn(t.z * sc, t.w * sc));
     } else if (!p_transpose) {
       float* o = static_cast<float*>(p_out) + static_cast<int64_t>(grow) * args.r + c4 * 4;
       *reinterpret_cast<float4*>(o) = make_float4(t.x * sc, t.y * sc, t.z * sc, t.w * sc);
     } else {
-      float* o = static_cast<float*>(p_out);
       const int64_t ld = p_rows;
+      float* o = static_cast<float*>(p_out) + static_cast<int64_t>(kRng ? p_group * p_ranks : 0) * ld;
       o[static_cast<int64_t>(c4 * 4 + 0) * ld + grow] = t.x * sc;
       o[static_cast<int64_t>(c4 * 4 + 1) * ld + grow] = t.y * sc;
       o[static_cast<int64_t>(c4 * 4 + 2) * ld + grow] = t.z * sc;

@@ -1,0 +1,79 @@
+// philox.cuh -- the keep mask of counter-based LoRA dropout.
+//
+// Philox4x32 (J. Salmon, M. Moraes, R. Dror and D. Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", SC 2011) with 7 rounds, the fewest that the
+// paper finds to pass its statistical tests.  The key is the 64-bit seed, the
+// counter (column / 8, row, offset low, offset high); 16-bit half i of the
+// four words (word i / 2, low half first) decides column 8 (column / 8) + i:
+// it is dropped when the half is below T = rint(65536 p).  A value therefore
+// depends on (seed, offset, row, column) alone, so that the forward and every
+// kernel of the backward draw the same mask and none is stored.
+//
+// Cost: 7 rounds of two 32 x 32 -> 64 multiplications and two 3-input xors per
+// 8 values, about 7 instructions per value with the comparisons.
+#pragma once
+
+#include "common.cuh"
+
+namespace qnf4 {
+
+struct DropoutRng {
+  const uint64_t* state;    // {seed, offset}
+  uint32_t threshold;       // T
+};
+
+struct PhiloxKey { uint32_t k0, k1, c2, c3; };
+
+__device__ __forceinline__ PhiloxKey philox_key(const uint64_t* state) {
+  const uint64_t seed = __ldg(reinterpret_cast<const unsigned long long*>(state));
+  const uint64_t off = __ldg(reinterpret_cast<const unsigned long long*>(state) + 1);
+  return PhiloxKey{static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32), static_cast<uint32_t>(off),
+                   static_cast<uint32_t>(off >> 32)};
+}
+
+// Keep bits of columns 8 group .. 8 group + 7 of a row, bit i for column i.
+__device__ __forceinline__ uint32_t philox_keep8(const PhiloxKey& key, uint32_t threshold, uint32_t row,
+                                                 uint32_t group) {
+  uint32_t c0 = group, c1 = row, c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    const uint64_t a = static_cast<uint64_t>(0xD2511F53u) * c0, b = static_cast<uint64_t>(0xCD9E8D57u) * c2;
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c1 = static_cast<uint32_t>(b);
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c3 = static_cast<uint32_t>(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  const uint32_t w[4] = {c0, c1, c2, c3};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bits |= ((w[i] & 0xFFFFu) >= threshold ? 1u : 0u) << (2 * i);
+    bits |= ((w[i] >> 16) >= threshold ? 1u : 0u) << (2 * i + 1);
+  }
+  return bits;
+}
+
+// Keep bits of the 32 columns from group 8-column group on.
+__device__ __forceinline__ uint32_t philox_keep32(const PhiloxKey& key, uint32_t threshold, uint32_t row,
+                                                  uint32_t group) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bits |= philox_keep8(key, threshold, row, group + i) << (8 * i);
+  return bits;
+}
+
+// The mask as bits, [M, n / 8] (the layout of the calls that take a mask):
+// one 32-bit word per thread and step.  n % 32 == 0.  Bound by the integer
+// pipe (about 230 operations per word), not by its M n / 8 bytes.
+__global__ void __launch_bounds__(256) keep_bits_kernel(DropoutRng rng, int64_t M, int64_t n, uint32_t* bits) {
+  const PhiloxKey key = philox_key(rng.state);
+  const int words = static_cast<int>(n / 32);
+  for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i < words) bits[m * words + i] = philox_keep32(key, rng.threshold, static_cast<uint32_t>(m), 4u * i);
+  }
+}
+
+}  // namespace qnf4

@@ -2,8 +2,8 @@
 //   us[m][j] = bf16(scale_a sum_k x[m][k] A_a[j][k]),   a = ids[m]
 // ("QLoRA", llm-compass, 方法与公式: the B A x branch, per token).
 //
-// A tile of 128 tokens is multiplied by the rank rows of up to
-// floor(256 / r8) of its distinct adapters at once (r8 = r rounded up to 8;
+// A tile of 128 tokens is multiplied by the rank rows of a group of its
+// distinct adapters at once, at most floor(256 / r8) (r8 = r rounded up to 8;
 // UMMA 128 x N x 16, N <= 256, fp32 accumulation in tensor memory), and every
 // token keeps the r columns of its own adapter.  The other columns are wasted
 // work that the tensor cores do not notice: the kernel is bound by reading x
@@ -27,8 +27,7 @@ constexpr int kUuThreads = 160;               // TMA warp, MMA warp; five warps 
 constexpr int kUuRing = 4;
 constexpr int kUuATile = 128 * 64 * 2;        // 16 KB of x
 
-// Adapters per group, and the UMMA's N for them.
-__host__ __device__ constexpr int uu_group(int r8) { return 256 / r8; }
+// The UMMA's N for a group of adapters.
 __host__ __device__ constexpr int uu_cols(int adapters, int r8) { return (adapters * r8 + 15) / 16 * 16; }
 __host__ __device__ constexpr int uu_pitch(int N) { return N * 4 + 16; }
 __host__ __device__ constexpr int uu_smem_bytes(int N) {
@@ -45,6 +44,7 @@ struct SlotsUsArgs {
   int64_t n_adapters;
   int n_tickets;
   int M, K, r, r8;
+  int per;                  // adapters per group
   int groups;               // groups per token tile in the grid
   int N, n_alloc;           // columns of a full group, TMEM columns
   int stages_per_split;
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kUuThreads) slots_us_umma_kernel(const __grid_
   }
   int place;
   const int n_list = distinct_slots<128, 256>(my_id, reinterpret_cast<int32_t*>(smem), list, counts, place);
-  const int per = uu_group(args.r8);
+  const int per = args.per;
   const int first = group * per;                             // the group's adapters in the list
   const int n_ad = min(per, n_list - first);
   if (n_ad <= 0) return;                                     // every CTA of the cluster alike

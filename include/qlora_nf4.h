@@ -78,7 +78,9 @@ enum {
   QLORA_OP_LINEAR_BWD = 3,
   QLORA_OP_LINEAR_FWD_DROPOUT = 4,
   QLORA_OP_LINEAR_BWD_DROPOUT = 5,
-  QLORA_OP_LINEAR_FWD_SLOTS = 6
+  QLORA_OP_LINEAR_FWD_SLOTS = 6,
+  QLORA_OP_LINEAR_FWD_DROPOUT_RNG = 7,
+  QLORA_OP_LINEAR_BWD_DROPOUT_RNG = 8
 };
 
 /* A quantized weight: device pointers in the format described above. */
@@ -330,6 +332,49 @@ int qlora_linear_bwd_dropout(const uint16_t* dh, const uint16_t* x, const uint16
                              size_t workspace_bytes, void* stream);
 
 /*
+ * LoRA dropout whose mask is drawn where it is used (lora_dropout as above;
+ * the pages do not say how the mask is drawn).  The mask is a function of a
+ * 64-bit seed, a 64-bit offset and the value's row and column, so the forward
+ * and the backward draw the same one and none is stored, and a captured graph
+ * draws a new one whenever the program changes the two numbers between
+ * replays.
+ *
+ *   Generator: Philox4x32 with 7 rounds ("Parallel random numbers: as easy as
+ *   1, 2, 3", SC 2011), key = seed, counter = (column / 8, row, offset low
+ *   32 bits, offset high 32 bits); 16-bit half i of its four words, low half
+ *   of the first word first, decides column 8 (column / 8) + i, which is
+ *   dropped when the half is below T = rint(65536 p) (at most 65535).
+ *   p is thereby rounded to q = T / 65536, and 1 / (1 - q) is the scaling.
+ *
+ * qlora_dropout_keep_bits -- the mask as bits, for inspection or for the
+ *   calls above (linear_*_dropout with these bits and p = q compute the same
+ *   layer, up to the order of sums and dA's rounding of du).
+ * qlora_linear_fwd_dropout_rng, qlora_linear_bwd_dropout_rng -- as
+ *   qlora_linear_fwd_dropout and qlora_linear_bwd_dropout with that mask; the
+ *   backward must find the same {seed, offset} as the forward.  dA is formed
+ *   from du in full fp32 precision (three bf16 parts), not from bf16(du):
+ *   dA and dB are the fp32 sums of exact products to about 1e-6.
+ *
+ * rng        device uint64 [2] {seed, offset}, 8-byte aligned, read when the
+ *            kernels run
+ * p          drop probability, 0 <= p < 1
+ * keep_bits  device uint8 [M, n / 8] (written), 4-byte aligned; bit i % 8 of
+ *            byte i / 8 of a row keeps column i; n % 64 == 0
+ * workspace: qlora_workspace_size(QLORA_OP_LINEAR_FWD_DROPOUT_RNG /
+ *            _BWD_DROPOUT_RNG, M, in, out, r) bytes.
+ * Other arguments, rules and returns as the calls above; QLORA_ERR_INVALID_ARG
+ * for a null or misaligned rng.
+ */
+int qlora_dropout_keep_bits(const uint64_t* rng, double p, int64_t M, int64_t n, uint8_t* keep_bits, void* stream);
+int qlora_linear_fwd_dropout_rng(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, const uint16_t* A,
+                                 const uint16_t* B, int r, float alpha, const uint64_t* rng, double p, uint16_t* h,
+                                 uint16_t* us_out, void* workspace, size_t workspace_bytes, void* stream);
+int qlora_linear_bwd_dropout_rng(const uint16_t* dh, const uint16_t* x, const uint16_t* us, int64_t M,
+                                 const qlora_nf4_weight* w, const uint16_t* A, const uint16_t* B, int r, float alpha,
+                                 const uint64_t* rng, double p, uint16_t* dx, float* dA, float* dB, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
  * Grouped projections: n independent QLoRA linears issued together, e.g.
  * the seven projections of one decoder layer ("QLoRA", llm-compass, 实现要点:
  * target_modules q/k/v/o and gate/up/down).  One problem per projection:
@@ -461,7 +506,7 @@ int qlora_selftest_wait_timeout(void* stream);
  * "scale_mean_tree", "dq_scales", "dequantize", "gemm_fwd", "gemm_dx",
  * "gemv", "gemv_finalize", "lora_rowwise" (us), "lora_rowwise_du" (du),
  * "lora_colwise" (dA and dB), "merge_adapter", "dropout_dx", "token_slots",
- * "slots_us", "slots_gemm".  Events are created by the library on first use (host-side
+ * "slots_us", "slots_gemm", "keep_bits".  Events are created by the library on first use (host-side
  * CUDA objects, no device memory).  Not for use during stream capture.
  *
  * qlora_timing_enable: on != 0 enables, 0 disables; returns the previous state.

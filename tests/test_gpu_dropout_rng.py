@@ -1,0 +1,258 @@
+"""The layer with counter-based LoRA dropout on the GPU: the mask bit for bit,
+the layer against the fp64 oracle with that mask.
+
+Tolerances, per value, counted from the roundings that are made:
+  h    2^-8 (|h| + sum |us B|): h and us are rounded to bf16 once each
+  us   2^-8 |us|
+  dx   2^-8 (|dh W| + |dx| + sum |du A| k/(1-q)): the base product, du and dx
+       are rounded to bf16
+  dA, dB  no rounding below fp32
+and for every fp32 sum of n terms (n + 64) 2^-23 times the sum of their
+absolute values (an addition is off by at most one step; du's own sum enters
+dA), with 2 % on top for products of these terms.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_11_b200 as qmod
+from bit_nf4_quantized_11_b200 import synth
+from oracle import linear, nf4, philox
+from parity import to_np
+
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
+
+
+def rng_tensor(seed, offset):
+    return torch.tensor([seed, offset], dtype=torch.int64, device="cuda")
+
+
+@pytest.mark.parametrize("seed,offset,p,M,n", [
+    (0, 0, 0.05, 3, 64),
+    (-1, -2**63, 0.5, 2, 192),
+    (2**62 + 12345, 2**40 + 7, 0.3, 17, 128),
+    (5, 3, 0.0, 4, 64),
+    (5, 3, 0.99999999, 4, 64),
+    (9, 1, 0.1, 70000, 64),               # more rows than grid rows
+    (9, 1, 0.1, 1, 8256),                 # a row of more than 256 words
+])
+def test_keep_bits(cuda_lib, seed, offset, p, M, n):
+    got = cuda_lib.dropout_keep_bits(rng_tensor(seed, offset), p, M, n).cpu().numpy()
+    rows = np.arange(M) if M < 100 else np.array([0, 1, 65534, 65535, 69999])
+    for m in rows:
+        # row m of the oracle's mask alone
+        k = np.array([[((philox.philox4x32((g, int(m), offset & philox.MASK, (offset >> 32) & philox.MASK),
+                                           (seed & philox.MASK, (seed >> 32) & philox.MASK), 7)[i // 2]
+                         >> (16 * (i % 2))) & 0xFFFF) >= philox.threshold(p) for i in range(8)]
+                      for g in range(n // 8)])
+        assert np.array_equal(got[m], np.packbits(k, axis=1, bitorder="little")[:, 0])
+
+
+def run(q, M, n_in, n_out, r, alpha, p, seed=0, sample=None):
+    prob = synth.problem(M, n_in, n_out, r, seed=seed)
+    dev = torch.device("cuda")
+    rng = rng_tensor(seed * 77 + 3, seed)
+    w = q.quantize_nf4(prob["W"].to(dev))
+    x, A, B, dh = (prob[k].to(dev) for k in ("x", "A", "B", "dh"))
+    h, us = q.linear_fwd_dropout_rng(x, w, A, B, alpha, rng, p)
+    dx, dA, dB = q.linear_bwd_dropout_rng(dh, x, us, w, A, B, alpha, rng, p)
+    assert q.last_device_status() == 0
+
+    keep = linear.unpack_keep(q.dropout_keep_bits(rng, p, M, n_in).cpu().numpy(), n_in)
+    qo = nf4.quantize(prob["W"].numpy())
+    W = nf4.dequantize(qo["codes"], qo["q8"], qo["step2"], qo["mean"]).astype(np.float64)
+    xn, An, Bn, dhn, usn = (to_np(t) for t in (x, A, B, dh, us))
+    drop = philox.threshold(p) / 65536
+    s, inv = alpha / r, 1 / (1 - drop)
+    rows = np.arange(M) if sample is None else np.asarray(sample)
+    xd = xn * keep * inv
+
+    h_ref, u_ref = linear.linear_fwd_dropout(xn[rows], W, An, Bn, alpha, keep[rows], drop)
+    us_ref = s * u_ref
+    us_size = s * np.abs(xd[rows]) @ np.abs(An).T
+    g = lambda n: (n + 64) * 2.0 ** -23                                            # noqa: E731
+    us_tol = 1.02 * (2.0 ** -8 * np.abs(us_ref) + g(n_in) * us_size)
+    assert np.all(np.abs(usn[rows] - us_ref) <= us_tol)
+    low = us_tol @ np.abs(Bn).T
+    size = np.abs(xn[rows]) @ np.abs(W).T + np.abs(us_ref) @ np.abs(Bn).T
+    tol = 1.02 * (2.0 ** -8 * np.abs(h_ref) + low + g(n_in + r) * size)
+    err = np.abs(to_np(h)[rows] - h_ref)
+    assert np.all(err <= tol), ("h", (err / tol).max())
+
+    du = s * (dhn @ Bn)
+    du_size = s * np.abs(dhn) @ np.abs(Bn)
+    base, lowdx = dhn[rows] @ W, np.abs(du[rows]) @ np.abs(An) * keep[rows] * inv
+    dx_ref = base + (du[rows] @ An) * keep[rows] * inv
+    size = np.abs(dhn[rows]) @ np.abs(W) + (du_size[rows] @ np.abs(An)) * keep[rows] * inv
+    tol = 1.02 * (2.0 ** -8 * (np.abs(base) + np.abs(dx_ref) + lowdx) + g(n_out + r) * size)
+    err = np.abs(to_np(dx)[rows] - dx_ref)
+    assert np.all(err <= tol), ("dx", (err / tol).max())
+
+    dB_ref, dB_size = dhn.T @ usn, np.abs(dhn).T @ np.abs(usn)
+    err, tol = np.abs(to_np(dB) - dB_ref), 1.02 * g(M) * dB_size
+    assert np.all(err <= tol + 1e-300), ("dB", (err / tol).max())
+    dA_ref, dA_size = du.T @ xd, np.abs(du).T @ np.abs(xd)
+    tol = 1.02 * (g(M) * dA_size + g(n_out) * (du_size.T @ np.abs(xd)))
+    err = np.abs(to_np(dA) - dA_ref)
+    assert np.all(err <= tol + 1e-300), ("dA", (err / tol).max())
+    # the norm-wise error of the fp32 gradients
+    for got, ref in ((to_np(dA), dA_ref), (to_np(dB), dB_ref)):
+        n = np.linalg.norm(ref)
+        assert n == 0 or np.linalg.norm(got - ref) <= 4e-6 * n
+
+
+@pytest.mark.parametrize("M,n_in,n_out,r,alpha,p", [
+    (1, 64, 64, 1, 1.0, 0.5),            # the smallest layer
+    (3, 128, 192, 8, 16.0, 0.0),         # nothing dropped
+    (9, 1024, 768, 16, 32.0, 0.05),
+    (16, 192, 320, 5, 10.0, 0.3),        # rank not a multiple of 8
+    (17, 576, 320, 24, 24.0, 0.1),
+    (64, 512, 512, 8, 16.0, 0.05),
+    (129, 256, 768, 32, 8.0, 0.05),
+    (200, 256, 192, 136, 16.0, 0.2),     # two column groups of the gradient
+    (256, 640, 256, 64, 64.0, 0.25),
+    (257, 320, 576, 80, 16.0, 0.5),
+    (300, 640, 320, 12, 24.0, 0.1),
+    (1500, 512, 448, 16, 32.0, 0.05),    # stages take turns over the accumulators
+    (70, 256, 192, 256, 16.0, 0.1),      # the largest rank: four column groups
+    (5000, 128, 192, 88, 16.0, 0.1),
+])
+def test_layer(cuda_lib, M, n_in, n_out, r, alpha, p):
+    run(cuda_lib, M, n_in, n_out, r, alpha, p, seed=M)
+
+
+def test_full_size_7b_attention(cuda_lib):
+    rng = np.random.default_rng(0)
+    run(cuda_lib, 4096, 4096, 4096, 16, 32.0, 0.05, seed=1, sample=np.sort(rng.choice(4096, 32, replace=False)))
+
+
+@pytest.mark.parametrize("M", [7, 200, 600])
+def test_equals_the_layer_with_that_mask(cuda_lib, M):
+    """The stored-mask calls with the mask as bits and the rounded p: the same
+    us up to the order of its sum, and gradients up to their bf16 du."""
+    q = cuda_lib
+    prob = synth.problem(M, 512, 384, 16, seed=M)
+    w = q.quantize_nf4(prob["W"].cuda())
+    x, A, B, dh = (prob[k].cuda() for k in ("x", "A", "B", "dh"))
+    rng, p = rng_tensor(11, M), 0.1
+    bits = q.dropout_keep_bits(rng, p, M, 512)
+    drop = philox.threshold(p) / 65536
+    h0, us0 = q.linear_fwd_dropout(x, w, A, B, 32.0, bits, drop)
+    h1, us1 = q.linear_fwd_dropout_rng(x, w, A, B, 32.0, rng, p)
+    assert (us0.float() - us1.float()).abs().max() <= 2.0 ** -7 * us0.float().abs().max()
+    g0 = q.linear_bwd_dropout(dh, x, us0, w, A, B, 32.0, bits, drop)
+    g1 = q.linear_bwd_dropout_rng(dh, x, us0, w, A, B, 32.0, rng, p)
+    for a, b in zip((h0,) + g0, (h1,) + g1):
+        assert (a.float() - b.float()).norm() <= 2.0 ** -7 * a.float().norm()
+
+
+def test_gradient_against_differences(cuda_lib):
+    """The layer is linear in A and in B: L(A) - L(0) = <dA, A> for
+    L = sum dh h, and with us from the forward L(B) - L(0) = <dB, B>.  dh = h
+    keeps L free of cancellation, so that the bf16 roundings of h (2^-8 each
+    side) bound the difference by 2^-7 of L's terms."""
+    q = cuda_lib
+    prob = synth.problem(400, 256, 320, 16, seed=5)
+    w = q.quantize_nf4(prob["W"].cuda())
+    x, A, B = (prob[k].cuda() for k in ("x", "A", "B"))
+    rng, p, alpha = rng_tensor(1, 2), 0.2, 16 * 64.0            # the adapter outweighs the base
+    h, us = q.linear_fwd_dropout_rng(x, w, A, B, alpha, rng, p)
+    zero, _ = q.linear_fwd_dropout_rng(x, w, torch.zeros_like(A), B, alpha, rng, p)
+    dx, dA, dB = q.linear_bwd_dropout_rng(h, x, us, w, A, B, alpha, rng, p)
+    diff = (h.double() * (h.double() - zero.double())).sum()
+    size = (h.double().abs() * (h.double().abs() + zero.double().abs())).sum()
+    assert (diff - (dA.double() * A.double()).sum()).abs() <= 2.0 ** -7 * size
+    assert (diff - (dB.double() * B.double()).sum()).abs() <= 2.0 ** -7 * size
+    assert diff > 0.3 * size                                    # the bounds above say something
+    # x enters both products: L(x) - L(0) = <dx, x>
+    assert ((h.double() ** 2).sum() - (dx.double() * x.double()).sum()).abs() <= 2.0 ** -6 * size
+
+
+@pytest.mark.parametrize("M", [5, 100, 700])
+def test_graph_draws_a_new_mask_when_the_state_changes(cuda_lib, M):
+    q = cuda_lib
+    prob = synth.problem(M, 512, 384, 16, seed=M)
+    w = q.quantize_nf4(prob["W"].cuda())
+    x, A, B, dh = (prob[k].cuda() for k in ("x", "A", "B", "dh"))
+    rng = rng_tensor(3, 4)
+
+    def step():
+        h, us = q.linear_fwd_dropout_rng(x, w, A, B, 32.0, rng, 0.2)
+        return (h, us) + q.linear_bwd_dropout_rng(dh, x, us, w, A, B, 32.0, rng, 0.2)
+    first = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, out))
+    rng[1] += 1
+    graph.replay()
+    torch.cuda.synchronize()
+    again = step()
+    assert all(torch.equal(a, b) for a, b in zip(again, out))
+    assert not torch.equal(first[1], out[1])
+    assert q.last_device_status() == 0
+
+
+def test_train_two_adapters_then_serve_them(cuda_lib):
+    """As they are used together: steps with dropout on two adapters of one
+    base, then one batch of requests over both, each token as its adapter's
+    layer alone gives it (bf16 h: one step apart at most)."""
+    q = cuda_lib
+    prob = synth.problem(320, 256, 384, 16, seed=8)
+    w = q.quantize_nf4(prob["W"].cuda())
+    x, A0, B0, dh = (prob[k].cuda() for k in ("x", "A", "B", "dh"))
+    tables_a, tables_b = [], []
+    for seed in (1, 2):
+        A, B = A0.float().clone(), B0.float().clone()
+        for step in range(3):
+            a16, b16 = A.bfloat16(), B.bfloat16()
+            rng = rng_tensor(seed, step)
+            h, us = q.linear_fwd_dropout_rng(x, w, a16, b16, 32.0, rng, 0.05)
+            _, dA, dB = q.linear_bwd_dropout_rng(dh, x, us, w, a16, b16, 32.0, rng, 0.05)
+            A -= 1e-4 * dA
+            B -= 1e-4 * dB
+        tables_a.append(A.bfloat16())
+        tables_b.append(B.bfloat16())
+    ids = q.token_slots(torch.tensor([100, 0, 120], dtype=torch.int32, device="cuda"),
+                        torch.tensor([1, 0, 0], dtype=torch.int32, device="cuda"), 230)
+    scale = torch.full((2,), 2.0, device="cuda")
+    y = q.linear_fwd_slots(x[:230].contiguous(), w, torch.stack(tables_a), torch.stack(tables_b), scale, ids)
+    for a, rows in ((1, slice(0, 100)), (0, slice(100, 220))):
+        ref, _ = q.linear_fwd(x[rows].contiguous(), w, tables_a[a], tables_b[a], 32.0)
+        tol = 2.0 ** -7 * ref.float().abs() + 2.0 ** -8 * ref.float().abs().max() * 2.0 ** -4
+        assert bool(((y[rows].float() - ref.float()).abs() <= tol).all())
+    base, _ = q.linear_fwd(x[220:230].contiguous(), w, torch.zeros_like(A0), B0, 32.0)
+    assert (y[220:230].float() - base.float()).norm() <= 2.0 ** -7 * base.float().norm()
+
+
+def test_python_refusals(cuda_lib):
+    q = cuda_lib
+    prob = synth.problem(8, 128, 64, 8, seed=1)
+    w = q.quantize_nf4(prob["W"].cuda())
+    x, A, B, dh = (prob[k].cuda() for k in ("x", "A", "B", "dh"))
+    rng = rng_tensor(1, 2)
+    for bad in (rng.cpu(), rng.int(), rng[:1], 7):
+        with pytest.raises((TypeError, ValueError)):
+            q.linear_fwd_dropout_rng(x, w, A, B, 8.0, bad, 0.1)
+        with pytest.raises((TypeError, ValueError)):
+            q.dropout_keep_bits(bad, 0.1, 8, 128)
+    for p in (-0.1, 1.0, float("nan")):
+        with pytest.raises(q.QLoRAError):
+            q.linear_fwd_dropout_rng(x, w, A, B, 8.0, rng, p)
+        with pytest.raises(q.QLoRAError):
+            q.dropout_keep_bits(rng, p, 8, 128)
+    with pytest.raises(q.QLoRAError):
+        q.dropout_keep_bits(rng, 0.1, 8, 72)
+    h, us = q.linear_fwd_dropout_rng(x, w, A, B, 8.0, rng, 0.1)
+    with pytest.raises(ValueError):
+        q.linear_bwd_dropout_rng(dh, x, us[:4], w, A, B, 8.0, rng, 0.1)
+    assert qmod.dropout_keep_bits(rng, 0.1, 0, 64).numel() == 0
