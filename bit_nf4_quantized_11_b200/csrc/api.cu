@@ -1136,10 +1136,13 @@ float kept_share(const qnf4::DropoutRng& rng) { return 1.f - static_cast<float>(
 // Tensor-memory columns of an rng rank-r launch: the SM's 512 shared by the
 // CTAs that its shared memory holds at once (a CTA that waited for another's
 // columns while both wait for their clusters could not finish).
-int lr_rng_alloc(int N, bool b_mn_major, int ring) {
+// All of it when there is at most one CTA per SM to run anyway.
+int lr_rng_alloc(int N, bool b_mn_major, int ring, int64_t ctas) {
   const int resident = 228 * 1024 / (qnf4::lr_smem_bytes(N, b_mn_major, ring) + 1024);
-  return resident <= 1 ? 512 : resident == 2 ? 256 : 128;
+  return resident <= 1 || ctas <= device_sm_count() ? 512 : resident == 2 ? 256 : 128;
 }
+
+int lr_rng_accumulators(int N, int n_alloc) { return std::max(1, std::min(8, n_alloc / ((N + 31) / 32 * 32))); }
 
 // us = bf16(s (x k) A^T) with the mask drawn.
 int launch_us_rng(const uint16_t* x, const uint16_t* A, uint16_t* us, int64_t M, int64_t in, int r, float s,
@@ -1157,7 +1160,7 @@ int launch_us_rng(const uint16_t* x, const uint16_t* A, uint16_t* us, int64_t M,
   const LrShape sh = lr_shape(tiles, stages, a.N, false);
   const int ks = std::min(sh.ks, 4);           // as with a stored mask (launch_lora_row)
   a.ring = sh.ring;
-  a.n_alloc = lr_rng_alloc(a.N, false, a.ring);
+  a.n_alloc = lr_rng_alloc(a.N, false, a.ring, static_cast<int64_t>(tiles) * ks);
   a.stages_per_split = static_cast<int>(cdiv(stages, ks));
   CUtensorMap tm[4];
   if (!make_tmap_bf16(&tm[0], x, M, in, 128) || !make_tmap_bf16(&tm[1], A, r, in, a.N)) return QLORA_ERR_CUDA;
@@ -1180,7 +1183,7 @@ int launch_du_parts(const uint16_t* dh, const uint16_t* B, uint16_t* du, int64_t
   const int64_t stages = cdiv(out, 64);
   const LrShape sh = lr_shape(tiles, stages, a.N, true);
   a.ring = sh.ring;
-  a.n_alloc = lr_rng_alloc(a.N, true, a.ring);
+  a.n_alloc = lr_rng_alloc(a.N, true, a.ring, static_cast<int64_t>(tiles) * sh.ks);
   a.stages_per_split = static_cast<int>(cdiv(stages, sh.ks));
   CUtensorMap tm[4];
   if (!make_tmap_bf16(&tm[0], dh, M, out, 128) || !make_tmap_bf16(&tm[1], B, out, r, 64)) return QLORA_ERR_CUDA;
@@ -1209,10 +1212,14 @@ int launch_grads_rng(const uint16_t* dh, const uint16_t* us, const uint16_t* x, 
   const LrShape sh = lr_shape(t_dB + t_dA, stages, a.N, true);
   int ks = sh.ks;
   a.ring = sh.ring;
-  a.n_alloc = lr_rng_alloc(a.N, true, a.ring);
-  // at most 32 stages (128 steps of the tensor cores' sum) per CTA and accumulator
-  const int n_acc = std::max(1, std::min(8, a.n_alloc / ((a.N + 31) / 32 * 32)));
-  while (ks < 8 && cdiv(stages, ks) > 32 * n_acc) ks *= 2;
+  const int64_t tiles = t_dB + t_dA;
+  a.n_alloc = lr_rng_alloc(a.N, true, a.ring, tiles * ks);
+  // at most 8 stages (32 steps of the tensor cores' sum) per accumulator, as
+  // far as the cluster goes
+  while (ks < 8 && cdiv(stages, ks) > 8 * lr_rng_accumulators(a.N, a.n_alloc)) {
+    ks *= 2;
+    a.n_alloc = lr_rng_alloc(a.N, true, a.ring, tiles * ks);
+  }
   a.stages_per_split = static_cast<int>(cdiv(stages, ks));
   CUtensorMap tm[4];
   if (!make_tmap_bf16(&tm[0], dh, M, out, 64) || !make_tmap_bf16(&tm[1], us, M, r, 64) ||

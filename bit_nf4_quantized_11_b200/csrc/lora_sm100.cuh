@@ -308,15 +308,39 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     };
     PhiloxKey key{};
     if (kRng) key = philox_key(args.rng.state);
-    // the 32 keep bits of item h of stage `it`, drawn (past the tokens or
-    // features nothing reads them)
-    auto draw_keep = [&](int it, int h) -> uint32_t {
-      const int j = t + MT * h, i = j & (kLrTileRows - 1), q = j >> 7;
-      const int k0 = (st_begin + it) * 64;
-      const int tok = kCol ? k0 + (i & 63) : row0 + i;
-      const int f0 = kCol ? row0 + 64 * (i >> 6) : k0;
-      return philox_keep32(key, args.rng.threshold, static_cast<uint32_t>(tok), static_cast<uint32_t>(f0 / 8 + 4 * q));
-    };
+    if (kRng) {
+      // one item per thread (256 masking threads); its 32 values' masks are
+      // drawn before the stage lands (past the tokens or features nothing
+      // reads them)
+      const int i = t & (kLrTileRows - 1), q = t >> 7;
+      const int r = kCol ? (i & 63) : i;
+      const uint32_t row_off = (kCol ? (i >> 6) * 8192 : 0) + r * 128;
+      for (int it = 0; it < n_iter; ++it) {
+        const int s = it % S;
+        const int k0 = (st_begin + it) * 64;
+        const int tok = kCol ? k0 + (i & 63) : row0 + i;
+        const int f0 = kCol ? row0 + 64 * (i >> 6) : k0;
+        uint32_t drop[4][4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          philox_drop8(key, args.rng.threshold, static_cast<uint32_t>(tok), static_cast<uint32_t>(f0 / 8 + 4 * q + c),
+                       drop[c]);
+        wait(full + s, (it / S) & 1u);
+        if (*abort_flag) break;
+        const uint32_t rbase = smem_u32(a_ring + s * kLrAStage) + row_off;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t addr = rbase + ((((4 * q + c) ^ r) & 7) << 4);
+          uint32_t v[4];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(addr) : "memory");
+          sts_v4(addr, v[0] & ~drop[c][0], v[1] & ~drop[c][1], v[2] & ~drop[c][2], v[3] & ~drop[c][3]);
+        }
+        fence_proxy_async_smem();                                   // generic writes before the MMAs read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(masked + s);
+      }
+    }
     if (!kRng)
       for (int i = 2; i < 6; ++i) prefetch_keep(i);
     uint32_t kb_n1[4], kb_n2[4];
@@ -324,21 +348,16 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
       load_keep(0, kb_n1);
       load_keep(1, kb_n2);
     }
-    for (int it = 0; it < n_iter; ++it) {
+    for (int it = 0; !kRng && it < n_iter; ++it) {
       const int s = it % S;
       uint32_t kb[4];
-      if (kRng) {
-        kb[0] = draw_keep(it, 0);                                    // (256 masking threads: one item each)
-        kb[1] = kb[2] = kb[3] = 0;
-      } else {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          kb[h] = kb_n1[h];
-          kb_n1[h] = kb_n2[h];
-        }
-        load_keep(it + 2, kb_n2);
-        prefetch_keep(it + 6);
+      for (int h = 0; h < 4; ++h) {
+        kb[h] = kb_n1[h];
+        kb_n1[h] = kb_n2[h];
       }
+      load_keep(it + 2, kb_n2);
+      prefetch_keep(it + 6);
       wait(full + s, (it / S) & 1u);
       if (*abort_flag) break;
       const uint32_t a_base = smem_u32(a_ring + s * kLrAStage);

@@ -31,9 +31,9 @@ __device__ __forceinline__ PhiloxKey philox_key(const uint64_t* state) {
                    static_cast<uint32_t>(off >> 32)};
 }
 
-// Keep bits of columns 8 group .. 8 group + 7 of a row, bit i for column i.
-__device__ __forceinline__ uint32_t philox_keep8(const PhiloxKey& key, uint32_t threshold, uint32_t row,
-                                                 uint32_t group) {
+// The four words for columns 8 group .. 8 group + 7 of a row: the low half of
+// word i decides column 2 i, the high half column 2 i + 1.
+__device__ __forceinline__ void philox_words(const PhiloxKey& key, uint32_t row, uint32_t group, uint32_t (&w)[4]) {
   uint32_t c0 = group, c1 = row, c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
 #pragma unroll
   for (int i = 0; i < 7; ++i) {
@@ -45,7 +45,25 @@ __device__ __forceinline__ uint32_t philox_keep8(const PhiloxKey& key, uint32_t 
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
-  const uint32_t w[4] = {c0, c1, c2, c3};
+  w[0] = c0; w[1] = c1; w[2] = c2; w[3] = c3;
+}
+
+// Those columns as bf16x2 masks of the dropped values (all ones in a dropped
+// half): half - T is negative exactly when the half is dropped, and a prmt
+// that replicates signs widens the two signs to halves.
+__device__ __forceinline__ void philox_drop8(const PhiloxKey& key, uint32_t threshold, uint32_t row, uint32_t group,
+                                             uint32_t (&drop)[4]) {
+  uint32_t w[4];
+  philox_words(key, row, group, w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) drop[i] = prmt((w[i] & 0xFFFFu) - threshold, (w[i] >> 16) - threshold, 0xFFBBu);
+}
+
+// Keep bits of columns 8 group .. 8 group + 7 of a row, bit i for column i.
+__device__ __forceinline__ uint32_t philox_keep8(const PhiloxKey& key, uint32_t threshold, uint32_t row,
+                                                 uint32_t group) {
+  uint32_t w[4];
+  philox_words(key, row, group, w);
   uint32_t bits = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -55,7 +73,7 @@ __device__ __forceinline__ uint32_t philox_keep8(const PhiloxKey& key, uint32_t 
   return bits;
 }
 
-// Keep bits of the 32 columns from group 8-column group on.
+// Keep bits of the 32 columns from 8-column group `group` on.
 __device__ __forceinline__ uint32_t philox_keep32(const PhiloxKey& key, uint32_t threshold, uint32_t row,
                                                   uint32_t group) {
   uint32_t bits = 0;
