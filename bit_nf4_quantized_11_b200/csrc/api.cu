@@ -520,7 +520,7 @@ int launch_gemm_pair(const qnf4::GemmArgs& args, const CUtensorMap& tm_act, cons
   const int64_t pairs = cdiv(args.M, Cfg::BM) * cdiv(args.N, Cfg::BN);
   {
     LaunchTimer lt_(kDx ? "gemm_dx" : "gemm_fwd", st);
-    kern<<<static_cast<unsigned>(2 * pairs), Cfg::THREADS, Cfg::SMEM, st>>>(tm_act, tm_lora, args, qnf4::PairSlots{});
+    kern<<<static_cast<unsigned>(2 * pairs), Cfg::THREADS, Cfg::SMEM, st>>>(tm_act, tm_lora, args, qnf4::PairExtra{});
   }
   QLORA_CUDA_TRY(cudaGetLastError());
   return QLORA_OK;
@@ -1116,7 +1116,7 @@ int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* 
     {
       LaunchTimer lt_("slots_gemm", st);
       kern<<<static_cast<unsigned>(2 * pairs), Cfg::THREADS, Cfg::SLOTS_SMEM, st>>>(
-          tm_act, tm_act, gemm_args(w, M, in, B, r, h, out), qnf4::PairSlots{ids, us, n_adapters, r8});
+          tm_act, tm_act, gemm_args(w, M, in, B, r, h, out), qnf4::PairExtra{ids, us, n_adapters, r8, {}, 0.f});
     }
     QLORA_CUDA_TRY(cudaGetLastError());
     return QLORA_OK;
@@ -1297,8 +1297,35 @@ int linear_fwd_rng_any_rank(const uint16_t* x, int64_t M, const qlora_nf4_weight
   return rc;
 }
 
+// dx = dh W0 + (du A) k / (1 - q) in one launch on CTA pairs; du in parts, of
+// which the tail reads the first columns (one column group).
+int launch_gemm_pair_drop(const qlora_nf4_weight* w, const uint16_t* dh, int64_t M, const uint16_t* du,
+                          const uint16_t* A, int r, uint16_t* dx, const qnf4::DropoutRng& rng, float inv_keep,
+                          cudaStream_t st) {
+  using Cfg = qnf4::PairCfg;
+  const int64_t in = w->cols, out = w->rows;
+  CUtensorMap tm_dh, tm_du;
+  if (!make_tmap_bf16(&tm_dh, dh, static_cast<uint64_t>(M), static_cast<uint64_t>(out)) ||
+      !make_tmap_bf16(&tm_du, du, static_cast<uint64_t>(M), static_cast<uint64_t>(qnf4::lr_part_cols(r))))
+    return QLORA_ERR_CUDA;
+  const auto kern = qnf4::qlora_gemm_pair_kernel<true, false, true>;
+  QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), Cfg::SMEM));
+  qnf4::PairExtra extra{};
+  extra.rng = rng;
+  extra.inv_keep = inv_keep;
+  const int64_t pairs = cdiv(M, Cfg::BM) * cdiv(in, Cfg::BN);
+  {
+    LaunchTimer lt_("gemm_dx", st);
+    kern<<<static_cast<unsigned>(2 * pairs), Cfg::THREADS, Cfg::SMEM, st>>>(
+        tm_dh, tm_du, gemm_args(w, M, out, A, r, dx, in), extra);
+  }
+  QLORA_CUDA_TRY(cudaGetLastError());
+  return QLORA_OK;
+}
+
 // Backward after validation, rank a multiple of 8; the streams as in
-// linear_bwd_impl with a mask.
+// linear_bwd_impl with a mask, except that on CTA pairs (and one column group
+// of du) the masked term is part of the dx GEMM, which then waits for du.
 int linear_bwd_rng_impl(const uint16_t* dh, const uint16_t* x, const uint16_t* us, int64_t M,
                         const qlora_nf4_weight* w, const uint16_t* A, const uint16_t* B, int r, float s,
                         const qnf4::DropoutRng& rng, uint16_t* dx, float* dA, float* dB, uint16_t* du,
@@ -1312,12 +1339,17 @@ int linear_bwd_rng_impl(const uint16_t* dh, const uint16_t* x, const uint16_t* u
   QLORA_CUDA_TRY(cudaEventRecord(g.ev[0], st));
   QLORA_CUDA_TRY(cudaStreamWaitEvent(g.hi, g.ev[0], 0));
   QLORA_CUDA_TRY(cudaStreamWaitEvent(g.lo, g.ev[0], 0));
-  int rc = launch_gemm(true, w, dh, M, out, nullptr, nullptr, 0, dx, in, g.hi);          // dx = dh W0
+  // below 1024 tokens the pass over dx costs less than waiting for du (512
+  // tokens of 4096 x 4096: 65 us apart, 68 in one; 4096 tokens: 160 and 153)
+  const bool fused = gemm_tile_m(M) == 512 && M >= 1024 && qnf4::lr_groups(r) == 1;
+  int rc = QLORA_OK;
+  if (!fused) rc = launch_gemm(true, w, dh, M, out, nullptr, nullptr, 0, dx, in, g.hi);  // dx = dh W0
   if (rc == QLORA_OK) rc = launch_du_parts(dh, B, du, M, out, r, s, g.lo);              // du = s dh B
   if (rc == QLORA_OK && cudaEventRecord(g.ev[1], g.lo) != cudaSuccess) rc = QLORA_ERR_CUDA;
-  if (rc == QLORA_OK) rc = launch_grads_rng(dh, us, x, du, M, in, out, r, dB, dA, inv_keep, rng, g.lo);
   if (rc == QLORA_OK && cudaStreamWaitEvent(g.hi, g.ev[1], 0) != cudaSuccess) rc = QLORA_ERR_CUDA;
-  if (rc == QLORA_OK) {
+  if (rc == QLORA_OK && fused) rc = launch_gemm_pair_drop(w, dh, M, du, A, r, dx, rng, inv_keep, g.hi);
+  if (rc == QLORA_OK) rc = launch_grads_rng(dh, us, x, du, M, in, out, r, dB, dA, inv_keep, rng, g.lo);
+  if (rc == QLORA_OK && !fused) {
     const int64_t tiles = cdiv(M, qnf4::kDxTileRows) * cdiv(in, qnf4::kDxTileCols);
     const int smem = qnf4::dx_smem_bytes(r);
     if (set_max_smem(reinterpret_cast<const void*>(qnf4::dropout_dx_kernel<true>), smem) != cudaSuccess) {

@@ -18,7 +18,6 @@
 #pragma once
 
 #include "common.cuh"
-#include "gemm_slots_sm100.cuh"   // tmem_ld_32x32b_x16
 #include "slots.cuh"
 
 namespace qnf4 {
