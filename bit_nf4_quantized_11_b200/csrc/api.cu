@@ -1339,9 +1339,7 @@ int linear_bwd_rng_impl(const uint16_t* dh, const uint16_t* x, const uint16_t* u
   QLORA_CUDA_TRY(cudaEventRecord(g.ev[0], st));
   QLORA_CUDA_TRY(cudaStreamWaitEvent(g.hi, g.ev[0], 0));
   QLORA_CUDA_TRY(cudaStreamWaitEvent(g.lo, g.ev[0], 0));
-  // below 1024 tokens the pass over dx costs less than waiting for du (512
-  // tokens of 4096 x 4096: 65 us apart, 68 in one; 4096 tokens: 160 and 153)
-  const bool fused = gemm_tile_m(M) == 512 && M >= 1024 && qnf4::lr_groups(r) == 1;
+  const bool fused = qnf4::lr_groups(r) == 1;
   int rc = QLORA_OK;
   if (!fused) rc = launch_gemm(true, w, dh, M, out, nullptr, nullptr, 0, dx, in, g.hi);  // dx = dh W0
   if (rc == QLORA_OK) rc = launch_du_parts(dh, B, du, M, out, r, s, g.lo);              // du = s dh B
@@ -1835,7 +1833,7 @@ int qlora_dropout_keep_bits(const uint64_t* rng, double p, int64_t M, int64_t n,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   {
     LaunchTimer lt_("keep_bits", st);
-    const dim3 grid(static_cast<unsigned>(cdiv(n / 32, 256)), static_cast<unsigned>(std::min<int64_t>(M, 65535)));
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cdiv(M * (n / 32), 256), device_sm_count() * 64));
     qnf4::keep_bits_kernel<<<grid, 256, 0, st>>>(dropout_rng(rng, p), M, n, reinterpret_cast<uint32_t*>(keep_bits));
   }
   QLORA_CUDA_TRY(cudaGetLastError());

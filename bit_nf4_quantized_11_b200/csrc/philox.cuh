@@ -59,18 +59,24 @@ __device__ __forceinline__ void philox_drop8(const PhiloxKey& key, uint32_t thre
   for (int i = 0; i < 4; ++i) drop[i] = prmt((w[i] & 0xFFFFu) - threshold, (w[i] >> 16) - threshold, 0xFFBBu);
 }
 
+// The drop bits of columns 8 group .. 8 group + 7, shifted into `bits` from
+// below (column 8 group + 7 first): the sign of half - T, one funnel shift each.
+__device__ __forceinline__ uint32_t philox_shift8(const PhiloxKey& key, uint32_t threshold, uint32_t row,
+                                                  uint32_t group, uint32_t bits) {
+  uint32_t w[4];
+  philox_words(key, row, group, w);
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    bits = __funnelshift_l((w[i] >> 16) - threshold, bits, 1);
+    bits = __funnelshift_l((w[i] & 0xFFFFu) - threshold, bits, 1);
+  }
+  return bits;
+}
+
 // Keep bits of columns 8 group .. 8 group + 7 of a row, bit i for column i.
 __device__ __forceinline__ uint32_t philox_keep8(const PhiloxKey& key, uint32_t threshold, uint32_t row,
                                                  uint32_t group) {
-  uint32_t w[4];
-  philox_words(key, row, group, w);
-  uint32_t bits = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    bits |= ((w[i] & 0xFFFFu) >= threshold ? 1u : 0u) << (2 * i);
-    bits |= ((w[i] >> 16) >= threshold ? 1u : 0u) << (2 * i + 1);
-  }
-  return bits;
+  return ~philox_shift8(key, threshold, row, group, 0u) & 0xFFu;
 }
 
 // Keep bits of the 32 columns from 8-column group `group` on.
@@ -78,19 +84,21 @@ __device__ __forceinline__ uint32_t philox_keep32(const PhiloxKey& key, uint32_t
                                                   uint32_t group) {
   uint32_t bits = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) bits |= philox_keep8(key, threshold, row, group + i) << (8 * i);
-  return bits;
+  for (int i = 3; i >= 0; --i) bits = philox_shift8(key, threshold, row, group + i, bits);
+  return ~bits;
 }
 
 // The mask as bits, [M, n / 8] (the layout of the calls that take a mask):
 // one 32-bit word per thread and step.  n % 32 == 0.  Bound by the integer
-// pipe (about 230 operations per word), not by its M n / 8 bytes.
+// pipe (about 260 operations per word), not by its M n / 8 bytes.
 __global__ void __launch_bounds__(256) keep_bits_kernel(DropoutRng rng, int64_t M, int64_t n, uint32_t* bits) {
   const PhiloxKey key = philox_key(rng.state);
-  const int words = static_cast<int>(n / 32);
-  for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i < words) bits[m * words + i] = philox_keep32(key, rng.threshold, static_cast<uint32_t>(m), 4u * i);
+  const int64_t words = n / 32, total = M * words;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < total;
+       e += static_cast<int64_t>(gridDim.x) * 256) {
+    // (total below 2^32: a 32-bit division)
+    const int64_t m = total <= 0xFFFFFFFFll ? static_cast<uint32_t>(e) / static_cast<uint32_t>(words) : e / words;
+    bits[e] = philox_keep32(key, rng.threshold, static_cast<uint32_t>(m), static_cast<uint32_t>(4 * (e - m * words)));
   }
 }
 
