@@ -951,10 +951,11 @@ bool slots_us_per_token(int64_t M, int64_t n_adapters, int r8) {
   return M <= kSlotsFewTokens && (M * r8 < 4096 || 16 * n_adapters >= M);
 }
 
-// Workspace of linear_fwd_slots: us [M, r8] bf16, and for few tokens the row
-// tiles' tickets and the fp32 partials of tiles cut between CTAs.
+// Workspace of linear_fwd_slots: us [M, r8] bf16; for few tokens the row
+// tiles' tickets and the fp32 partials of tiles cut between CTAs, for more the
+// adapter lists of the token tiles.
 struct SlotsWs {
-  size_t ticket_off, part_off, total;
+  size_t ticket_off, part_off, tiles_off, total;
 };
 
 int slots_ctas(int64_t in, int64_t out) {
@@ -965,8 +966,11 @@ int slots_ctas(int64_t in, int64_t out) {
 SlotsWs slots_ws(int64_t M, int64_t in, int64_t out, int r) {
   SlotsWs w{};
   w.ticket_off = round256(static_cast<size_t>(M) * padded_rank(r) * 2);
-  w.total = w.part_off = w.ticket_off;
-  if (M > kSlotsFewTokens) return w;
+  w.total = w.part_off = w.tiles_off = w.ticket_off;
+  if (M > kSlotsFewTokens) {
+    w.total = w.tiles_off + round256(static_cast<size_t>(cdiv(M, qnf4::kSlotsTile)) * sizeof(qnf4::SlotsTile));
+    return w;
+  }
   w.part_off = w.ticket_off + round256(static_cast<size_t>(cdiv(out, qnf4::kSgRows)) * 4);
   const size_t N = static_cast<size_t>(cdiv(M, 16) * 16);
   w.total = w.part_off + static_cast<size_t>(slots_ctas(in, out)) * 2 * N * qnf4::kSgRows * 4;
@@ -975,7 +979,7 @@ SlotsWs slots_ws(int64_t M, int64_t in, int64_t out, int r) {
 
 int launch_slots_us(const uint16_t* x, const uint16_t* A, const float* scale, const int32_t* ids, int64_t M,
                     int64_t in, int64_t n_adapters, int r, uint16_t* us, uint32_t* tickets, int n_tickets,
-                    cudaStream_t st) {
+                    bool overlap, cudaStream_t st) {
   const int r8 = padded_rank(r);
   if (slots_us_per_token(M, n_adapters, r8)) {
     LaunchTimer lt_("slots_us", st);
@@ -1023,13 +1027,20 @@ int launch_slots_us(const uint16_t* x, const uint16_t* A, const float* scale, co
   cfg.blockDim = dim3(qnf4::kUuThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = static_cast<unsigned>(ks);
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  int n_attr = 0;
+  if (ks > 1) {
+    attr[n_attr].id = cudaLaunchAttributeClusterDimension;
+    attr[n_attr].val.clusterDim.x = 1;
+    attr[n_attr].val.clusterDim.y = static_cast<unsigned>(ks);
+    attr[n_attr++].val.clusterDim.z = 1;
+  }
+  if (overlap && !g_timing_on.load()) {          // (timed launches one after another)
+    attr[n_attr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n_attr++].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = ks > 1 ? 1 : 0;
+  cfg.numAttrs = n_attr;
   {
     LaunchTimer lt_("slots_us", st);
     QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, qnf4::slots_us_umma_kernel, tm_x, tm_a, a));
@@ -1103,8 +1114,15 @@ int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* 
   const int r8 = padded_rank(r);
   const bool few = M <= kSlotsFewTokens;
   uint32_t* tickets = few ? reinterpret_cast<uint32_t*>(base + ws.ticket_off) : nullptr;
+  qnf4::SlotsTile* tiles = reinterpret_cast<qnf4::SlotsTile*>(base + ws.tiles_off);
+  if (!few) {
+    LaunchTimer lt_("slots_tiles", st);
+    qnf4::slots_tiles_kernel<<<static_cast<unsigned>(cdiv(M, qnf4::kSlotsTile)), qnf4::kSlotsTile, 0, st>>>(
+        ids, M, n_adapters, r8, tiles);
+    QLORA_CUDA_TRY(cudaGetLastError());
+  }
   const int rc = launch_slots_us(x, A, scale, ids, M, in, n_adapters, r, us, tickets,
-                                 few ? static_cast<int>(cdiv(out, qnf4::kSgRows)) : 0, st);
+                                 few ? static_cast<int>(cdiv(out, qnf4::kSgRows)) : 0, !few, st);
   if (rc != QLORA_OK) return rc;
   if (!few) {
     using Cfg = qnf4::PairCfg;
@@ -1116,7 +1134,7 @@ int linear_fwd_slots_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* 
     {
       LaunchTimer lt_("slots_gemm", st);
       kern<<<static_cast<unsigned>(2 * pairs), Cfg::THREADS, Cfg::SLOTS_SMEM, st>>>(
-          tm_act, tm_act, gemm_args(w, M, in, B, r, h, out), qnf4::PairExtra{ids, us, n_adapters, r8, {}, 0.f});
+          tm_act, tm_act, gemm_args(w, M, in, B, r, h, out), qnf4::PairExtra{tiles, us, r8, {}, 0.f});
     }
     QLORA_CUDA_TRY(cudaGetLastError());
     return QLORA_OK;

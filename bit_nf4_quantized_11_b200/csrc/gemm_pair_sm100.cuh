@@ -30,9 +30,10 @@
 // Every wait is bounded (see gemm_sm100.cuh); no TMA multicast is used.
 //
 // kSlots: the forward with one adapter per token (h[m] = W0 x[m] + B_a us[m],
-// a = ids[m]).  The CTAs list the distinct adapters of their 512 tokens; the
-// rank columns of the listed adapters, one after another, are the K slices
-// behind the base's.  There the dequant groups write both operands: B_a rows
+// a = ids[m]).  A kernel before lists the distinct adapters of each tile of
+// 512 tokens (slots.cuh); the rank columns of the listed adapters, one after
+// another, are K slices before the base's (before: their loads then overlap
+// the filling of the pipeline).  There the dequant groups write both operands: B_a rows
 // as they are, and the token rows of us under the columns of the token's own
 // adapter with zeros elsewhere.  A B value that is infinite or NaN would reach
 // the other tokens through those zeros: it is carried as 0 and both CTAs are
@@ -69,15 +70,13 @@ struct PairCfg {
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int kGroups = 4;                    // dequant groups, one stage each in turn
   static constexpr int THREADS = 64 + kGroups * 128;   // 2 + 16 warps
-  // kSlots: per token its first rank column, the distinct adapters, counts
-  static constexpr int SLOTS_SMEM = SMEM + (2 * BM + 16) * 4;
+  static constexpr int SLOTS_SMEM = SMEM + BM * 4 + 16;   // kSlots: per token its first rank column; a flag
 };
 
 struct PairExtra {
   // kSlots
-  const int32_t* ids;       // [M]
+  const SlotsTile* tiles;   // per 512 tokens
   const uint16_t* us;       // [M, r8]
-  int64_t n_adapters;
   int r8;                   // r rounded up to 8
   // kDrop
   DropoutRng rng;
@@ -123,27 +122,24 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
   const int n_main = args.K / 64;
   const uint64_t tmo = args.timeout_ns;
   int32_t* tok_col = reinterpret_cast<int32_t*>(smem + Cfg::RING + 256);   // kSlots
-  int32_t* list = tok_col + Cfg::BM;
-  volatile int32_t* odd = list + Cfg::BM + 15;         // a B value of either CTA was not finite
-  int k_low = args.r;                                  // rank columns behind the base
+  volatile int32_t* odd = tok_col + Cfg::BM;           // a B value of either CTA was not finite
+  const int32_t* list = nullptr;                       // the tile's adapters
+  int k_low = args.r;                                  // rank columns beside the base
   int n_list = 0;
   if constexpr (kSlots) {
-    int32_t id = -1;
-    if (threadIdx.x < Cfg::BM && m0 + static_cast<int>(threadIdx.x) < args.M) {
-      id = __ldg(slots.ids + m0 + threadIdx.x);
-      if (id < 0 || id >= slots.n_adapters) id = -1;
-    }
-    int place;
-    // 16 counts: the list has room for 512, the counts lie behind it
-    __shared__ int32_t counts[Cfg::BM / 32];
-    n_list = distinct_slots<Cfg::BM, 2 * Cfg::BM>(id, reinterpret_cast<int32_t*>(smem), list, counts, place);
-    if (threadIdx.x < Cfg::BM) tok_col[threadIdx.x] = place < 0 ? -(1 << 29) : place * slots.r8;
+    const SlotsTile& tile = slots.tiles[tile_m];
+    n_list = __ldg(&tile.n);
+    list = tile.list;
+    if (threadIdx.x < Cfg::BM) tok_col[threadIdx.x] = __ldg(tile.col + threadIdx.x);
     if (threadIdx.x == 0) *odd = 0;
     k_low = n_list * slots.r8;
-    fence_proxy_async_smem();                          // the hash table before the copies over it
   }
   const int n_lora = (k_low + 63) / 64;
   const int n_iter = n_main + n_lora;
+  // the rank slices come behind the base's, with kSlots before them
+  auto is_low = [&](int it) { return kSlots ? it < n_lora : it >= n_main; };
+  auto main_of = [&](int it) { return kSlots ? it - n_lora : it; };
+  auto low_of = [&](int it) { return kSlots ? it : it - n_main; };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -189,7 +185,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
         const uint32_t ph = (it / kStages) & 1u;
         wait(empty + s, ph ^ 1u);
         if (*abort_flag) break;                           // a wait timed out: issue nothing more
-        if (kSlots && it >= n_main) {                     // the dequant groups write the token operand
+        if (kSlots && is_low(it)) {                       // the dequant groups write the token operand
           if (leader) mbar_arrive(full + s);
           ++issued;
           continue;
@@ -197,18 +193,18 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
         if (leader) mbar_arrive_expect_tx(full + s, 2 * Cfg::A_STAGE);    // both CTAs' bytes
         const uint32_t bar = mapa_shared(smem_u32(full + s), 0);
         const uint32_t dst = smem_u32(a_ring + s * Cfg::A_STAGE);
-        if (it + kStages < n_main) {                      // warm L2 for a later stage
+        if (main_of(it) + kStages < n_main) {             // warm L2 for a later stage
 #pragma unroll
           for (int sub = 0; sub < 2; ++sub)
-            tma_prefetch_l2_2d(&tm_act, (it + kStages) * 64, m0 + sub * 256 + static_cast<int>(rank) * 128);
+            tma_prefetch_l2_2d(&tm_act, (main_of(it) + kStages) * 64, m0 + sub * 256 + static_cast<int>(rank) * 128);
         }
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
           const int row = m0 + sub * 256 + static_cast<int>(rank) * 128;
-          if (it < n_main)
-            tma_load_2d_pair(dst + sub * Cfg::A_SUB, &tm_act, bar, it * 64, row);
+          if (!is_low(it))
+            tma_load_2d_pair(dst + sub * Cfg::A_SUB, &tm_act, bar, main_of(it) * 64, row);
           else
-            tma_load_2d_pair(dst + sub * Cfg::A_SUB, &tm_lora, bar, (it - n_main) * 64, row);
+            tma_load_2d_pair(dst + sub * Cfg::A_SUB, &tm_lora, bar, low_of(it) * 64, row);
         }
         ++issued;
       }
@@ -231,7 +227,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
         const uint32_t a_base = smem_u32(a_ring + s * Cfg::A_STAGE);
         const uint32_t b_base = smem_u32(b_ring + s * Cfg::B_STAGE);
         int ksteps = 4;
-        if (it >= n_main) ksteps = min(4, (k_low - (it - n_main) * 64 + 15) / 16);
+        if (is_low(it)) ksteps = min(4, (k_low - low_of(it) * 64 + 15) / 16);
         for (int kk = 0; kk < ksteps; ++kk) {
           const uint64_t bdesc = kDx ? umma_desc_sw128(b_base + kk * 2048, 8192, 1024)
                                      : umma_desc_sw128(b_base + kk * 32, 16, 1024);
@@ -317,9 +313,10 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
       float st;
     };
     auto load_stage = [&](int it, StageIn& d) {
-      if (col_valid && it < n_main) {
-        const uint8_t* p = code_ptr + it * code_step;
-        const int64_t blk = q8_idx + it * q8_step;
+      const int k = main_of(it);
+      if (col_valid && k >= 0 && k < n_main) {
+        const uint8_t* p = code_ptr + k * code_step;
+        const int64_t blk = q8_idx + k * q8_step;
         if (args.codes_32b) {
           ld_nc_v8(p, d.c0, d.c1);
         } else {
@@ -333,7 +330,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
 
     // Decode (or fetch the LoRA rows of) stage `it` into 8 x 16 B of registers.
     auto produce = [&](int it, const StageIn& in, uint4 (&v)[8]) {
-      if (it < n_main) {
+      if (!is_low(it)) {
         if (col_valid) {
           const float c_hat = block_scale(in.q, in.st, mu);
           const Nf4Table tb = make_table(args.L, c_hat);
@@ -350,14 +347,14 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
         }
       } else if constexpr (kSlots) {
         // rank columns [64 j, 64 j + 64) of the listed adapters, in chunks of 8
-        const int j = it - n_main;
+        const int j = low_of(it);
         int li = j * 64 / slots.r8, c0 = j * 64 - li * slots.r8;
         uint32_t exps = 0;                                // bit 15 or 31: an exponent of all ones
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           v[c] = make_uint4(0, 0, 0, 0);
           if (col_valid && li < n_list) {
-            const uint16_t* src = args.lora_w + (static_cast<int64_t>(list[li]) * args.N + lora_row) * args.r + c0;
+            const uint16_t* src = args.lora_w + (static_cast<int64_t>(__ldg(list + li)) * args.N + lora_row) * args.r + c0;
             if ((args.r & 7) == 0) {
               v[c] = ld_nc_v4(src);
             } else {
@@ -386,7 +383,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
             asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(mapa_shared(at, k)), "r"(1) : "memory");
         }
       } else {
-        const int j = it - n_main;
+        const int j = low_of(it);
         const uint16_t* src = nullptr;
         int count = 0;
         if (!kDx) {
@@ -429,9 +426,9 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
 #pragma unroll
       for (int c = 0; c < 8; ++c) sts_v4(dst + ((c ^ key) << 4), v[c].x, v[c].y, v[c].z, v[c].w);
       if constexpr (kSlots) {
-        if (it >= n_main) {
+        if (is_low(it)) {
           // token rows t of both sub-tiles: us under the columns of the token's adapter
-          const int e = it - n_main;
+          const int e = low_of(it);
 #pragma unroll
           for (int sub = 0; sub < 2; ++sub) {
             const int i = sub * 256 + static_cast<int>(rank) * 128 + t;         // of the 512 tokens

@@ -140,6 +140,37 @@ __device__ __forceinline__ int distinct_slots(int32_t id, int32_t* hash, int32_t
   return n;
 }
 
+// What the CTA-pair GEMM needs to know about each tile of 512 tokens: the
+// distinct adapters, and each token's first rank column among theirs (far
+// below 0 for none).  One CTA per tile, once per call: inside the GEMM every
+// wave of tiles would build the list again (about 2.5 us each).
+constexpr int kSlotsTile = 512;
+struct SlotsTile {
+  int32_t n;                             // adapters in the list
+  int32_t pad[3];
+  int32_t list[kSlotsTile];
+  int32_t col[kSlotsTile];
+};
+
+__global__ void __launch_bounds__(kSlotsTile) slots_tiles_kernel(const int32_t* __restrict__ ids, int64_t M,
+                                                                 int64_t n_adapters, int r8,
+                                                                 SlotsTile* __restrict__ tiles) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int32_t hash[4 * kSlotsTile], list[kSlotsTile], counts[kSlotsTile / 32];
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * kSlotsTile + threadIdx.x;
+  int32_t id = -1;
+  if (m < M) {
+    id = __ldg(ids + m);
+    if (id < 0 || id >= n_adapters) id = -1;
+  }
+  int place;
+  const int n = distinct_slots<kSlotsTile, 2 * kSlotsTile>(id, hash, list, counts, place);
+  SlotsTile& t = tiles[blockIdx.x];
+  t.col[threadIdx.x] = place < 0 ? -(1 << 29) : place * r8;
+  if (static_cast<int>(threadIdx.x) < n) t.list[threadIdx.x] = list[threadIdx.x];
+  if (threadIdx.x == 0) t.n = n;
+}
+
 // The products of an adapter row's infinite or NaN B values with a token's us.
 __device__ __noinline__ float slots_odd_term(const uint16_t* B_row, const uint16_t* us, int r) {
   float f = 0.f;

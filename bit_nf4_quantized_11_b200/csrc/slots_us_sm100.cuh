@@ -90,7 +90,12 @@ __global__ void __launch_bounds__(kUuThreads) slots_us_umma_kernel(const __grid_
   const int per = args.per;
   const int first = group * per;                             // the group's adapters in the list
   const int n_ad = min(per, n_list - first);
-  if (n_ad <= 0) return;                                     // every CTA of the cluster alike
+  // The kernel before (the tiles' adapter lists) may still run: what follows
+  // this one relies on it too, so no CTA leaves before it is done.
+  if (n_ad <= 0) {                                           // every CTA of the cluster alike
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   if (threadIdx.x < 128) tok_place[threadIdx.x] = place;
   const int cols = uu_cols(n_ad, args.r8);
   fence_proxy_async_smem();                                  // the hash table before the copies over it
@@ -211,6 +216,7 @@ __global__ void __launch_bounds__(kUuThreads) slots_us_umma_kernel(const __grid_
     *reinterpret_cast<uint2*>(args.us + static_cast<int64_t>(m0 + t) * args.r8 + c4) =
         make_uint2(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]));
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (ks > 1) cluster_sync_all();                            // no CTA leaves while others read it
   if (warp == 1) {
     tc_fence_after_sync();
