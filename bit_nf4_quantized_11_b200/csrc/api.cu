@@ -1080,10 +1080,9 @@ int launch_slots_gemm(const uint16_t* x, int64_t M, const qlora_nf4_weight* w, c
       !make_tmap_bf16_blocks(&tm_x, x, static_cast<uint64_t>(M), static_cast<uint64_t>(in),
                              static_cast<uint32_t>(a.N), static_cast<uint32_t>(qnf4::sg_kb(a.N))))
     return QLORA_ERR_CUDA;
-  const auto kern = a.N <= 32    ? qnf4::slots_gemm_kernel<4, 4, true>
-                    : a.N <= 64  ? qnf4::slots_gemm_kernel<4, 2, true>
-                    : a.N <= 128 ? qnf4::slots_gemm_kernel<2, 2, true>
-                                 : qnf4::slots_gemm_kernel<2, 2, false>;
+  const auto kern = a.N <= 64    ? qnf4::slots_gemm_kernel<4, true>
+                    : a.N <= 128 ? qnf4::slots_gemm_kernel<2, true>
+                                 : qnf4::slots_gemm_kernel<2, false>;
   const int smem = qnf4::sg_smem_bytes(a.N);
   QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), smem));
   cudaLaunchConfig_t cfg{};

@@ -68,9 +68,9 @@ constexpr int kSgGroups = 4;                  // dequant groups
 constexpr int kSgDecThreads = kSgGroups * 128;
 constexpr int kSgThreads = 256 + kSgDecThreads;
 
-// K blocks per stage, x stages in flight (64 KB, without the table 128 KB).
+// K blocks per stage; two x stages in flight (64 KB, without the table 128 KB).
 __host__ __device__ constexpr int sg_kb(int N) { return N <= 64 ? 4 : 2; }
-__host__ __device__ constexpr int sg_stages(int N) { return N <= 32 ? 4 : 2; }
+constexpr int kSgXStages = 2;
 __host__ __device__ constexpr bool sg_lut(int N) { return N <= 128; }
 // Shared memory by absolute shared address: the level table sits on a 64 KB
 // boundary (prmt assembles its addresses), x behind it; codes, scales, lists
@@ -79,14 +79,17 @@ constexpr uint32_t kSgTableAt = 0x10000;
 __host__ __device__ constexpr int sg_low_bytes() {
   return kSgUnits * (kSgCodeTile + kSgRows * 16) + 2 * kSgMaxN * 4 + kSgMaxCtas * 4 + 64 + 512;
 }
+// No other CTA of this library that allocates tensor memory fits beside this
+// one (the rank-r kernels take 72 KB or more): two that waited for each
+// other's columns while both wait for their clusters could not finish.
+constexpr int kSgMinSmem = 160 * 1024;
 __host__ __device__ constexpr int sg_smem_bytes(int N) {   // (the window starts at or above address 0)
-  return static_cast<int>(kSgTableAt) + (sg_lut(N) ? 65536 + sg_stages(N) * sg_kb(N) * N * 128 : 131072);
+  const int need = static_cast<int>(kSgTableAt) + (sg_lut(N) ? 65536 + kSgXStages * sg_kb(N) * N * 128 : 131072);
+  return need > kSgMinSmem ? need : kSgMinSmem;
 }
 static_assert(sg_low_bytes() + 1024 + 1024 <= static_cast<int>(kSgTableAt), "the low part fits below the table");
 static_assert(sg_smem_bytes(kSgMaxN) <= 227 * 1024 && sg_smem_bytes(128) <= 227 * 1024, "shared memory of a CTA");
-// No other CTA of this library that allocates tensor memory fits beside this
-// one (the rank-r kernels take 72 KB or more).
-static_assert(sg_smem_bytes(16) > (228 - 72) * 1024, "one CTA with tensor memory per SM");
+static_assert(kSgMinSmem > (228 - 72) * 1024, "one CTA with tensor memory per SM");
 
 struct SlotsGemmArgs {
   const int8_t* q8;
@@ -174,12 +177,14 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 // First unit of CTA c when T units are dealt out to G CTAs.
 __device__ __forceinline__ int64_t sg_unit_begin(int64_t c, int64_t T, int64_t G) { return T * c / G; }
 
-// KB, S, kLut: sg_kb(N), sg_stages(N), sg_lut(N).
-template <int KB, int S, bool kLut>
+// KB, kLut: sg_kb(N), sg_lut(N).
+template <int KB, bool kLut>
 __global__ void __launch_bounds__(kSgThreads, 1)
 slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_x,
                   const SlotsGemmArgs args) {
+  constexpr int S = kSgXStages;
   constexpr int SA = kSgABlocks / KB;                        // stages of the A ring
+  constexpr bool kOneRing = S == SA;                         // x and A slots are freed together
   constexpr int SPU = 4 / KB;                                // stages per unit
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -298,7 +303,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       for (int i = 0; i < n_u && ok; ++i) {
         for (int j = 0; j < SPU; ++j, ++it) {
           const int s = it % S;
-          if (!(ok = wait(xempty + s, ((it / S) & 1u) ^ 1u))) break;
+          if (!(ok = wait((kOneRing ? aempty : xempty) + s, ((it / S) & 1u) ^ 1u))) break;
           if (uu < UB) {
             mbar_arrive_expect_tx(xfull + s, static_cast<uint32_t>(x_stage));
             tma_load_3d(smem_u32(x_ring + s * x_stage), &tm_x, xfull + s, 0, 0, uu * 4 + j * KB);
@@ -341,7 +346,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
           acc = 1u;
         }
         umma_commit_elected(smem_u32(aempty + sa), elected);
-        umma_commit_elected(smem_u32(xempty + s), elected);
+        if (!kOneRing) umma_commit_elected(smem_u32(xempty + s), elected);
       }
       if (++uu == UPT || i == n_u - 1) {                     // the segment ends
         uu = 0;
@@ -455,35 +460,30 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       dph ^= 1u;
       return done;
     };
-    // The tensor-memory store of a block completes while the next one is being
-    // read: its arrive waits until then.
-    int stored = -1;                                         // A stage with a store under way
-    auto flush = [&]() {
-      if (stored < 0) return;
-      tmem_st_wait();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(afull + stored);
-      stored = -1;
-    };
     int uu = uu0, tile = tile0, seg = 0, cs = 0, seg_uu = uu0;
     uint32_t cph = 0;
     int cut_first = -1, cut_last = -1;                       // this CTA's cut tiles
+    // The codes and the scale of a unit's block are read while the store of the
+    // block before it completes.
+    uint32_t c[8];
+    float c_hat = 0.f;
+    auto read_codes = [&]() {
+      if (!wait_warp(sfull + cs, cph)) return false;
+      const uint32_t crow = smem_u32(c_ring + cs * kSgCodeTile) + t * 128;
+      lds_v4(crow + (((2 * g) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[0]));
+      lds_v4(crow + (((2 * g + 1) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[4]));
+      c_hat = s_ring[(cs * 4 + g) * kSgRows + t];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cempty + cs);
+      if (++cs == kSgUnits) { cs = 0; cph ^= 1u; }
+      return true;
+    };
     bool ok = true;
+    if (uu < UB) ok = read_codes();
     for (int i = 0; i < n_u && ok; ++i) {
       const int it = i * SPU + g / KB, sa = it % SA;
       uint32_t v[32];
       if (uu < UB) {
-        if (!(ok = wait_warp(sfull + cs, cph))) break;
-        const uint32_t crow = smem_u32(c_ring + cs * kSgCodeTile) + t * 128;
-        uint32_t c[8];
-        lds_v4(crow + (((2 * g) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[0]));
-        lds_v4(crow + (((2 * g + 1) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[4]));
-        const float c_hat = s_ring[(cs * 4 + g) * kSgRows + t];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(cempty + cs);
-        if (++cs == kSgUnits) { cs = 0; cph ^= 1u; }
-        flush();
         if (kLut) {
           uint64_t c2;
           asm("mov.b64 %0, {%1, %1};" : "=l"(c2) : "f"(c_hat));
@@ -516,7 +516,6 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
         const int e = (uu - UB) * 4 + g;
         const int row = tile * kSgRows + t;
         const bool row_ok = row < args.out;
-        flush();
         // the 8 chunks of this row's B values, all loads under way together
         int li = e * 64 / args.r8, j0 = e * 64 - li * args.r8;
 #pragma unroll
@@ -568,14 +567,17 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
         }
       }
       tmem_st_32x32b_x32(a_lane + (sa * KB + ib) * 32, v);
-      stored = sa;
+      if (i + 1 < n_u && (uu + 1 == UPT || uu + 1 < UB) && !(ok = read_codes())) break;
+      tmem_st_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(afull + sa);
       if (SA > S && uu < UB && !(ok = x_done(it))) break;
 
       if (++uu != UPT && i != n_u - 1) continue;
       // ---------------------------------------------------------- the segment ends
       const bool whole = seg_uu == 0 && uu == UPT;           // this CTA holds all of the tile
       const int n0 = tile * kSgRows;
-      flush();
       if (!(ok = wait_warp(acc_full, seg & 1u))) break;
       tc_fence_after_sync();
       const int my_odd = odd[seg & 1];
