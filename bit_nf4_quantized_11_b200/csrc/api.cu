@@ -598,8 +598,10 @@ int launch_lora_umma(const CUtensorMap (&tm)[4], const qnf4::LrArgs& a, int ks, 
                      cudaStream_t st) {
   auto kern = qnf4::lora_umma_kernel<kCol, kBMN, kRng>;
   int smem = qnf4::lr_smem_bytes(a.N, kBMN, a.ring);
-  // with all of the tensor memory, no other rank-r CTA (72 KB or more) beside it
+  // no other CTA with tensor memory (72 KB or more each) beside those that
+  // already share all 512 columns
   if (kRng && a.n_alloc == 512) smem = std::max(smem, 160 * 1024);
+  if (kRng && a.n_alloc == 256) smem = std::max(smem, 78 * 1024);
   QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(kern), smem));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid_x, static_cast<unsigned>(ks), 1);
@@ -1019,7 +1021,6 @@ int launch_slots_us(const uint16_t* x, const uint16_t* A, const float* scale, co
       !make_tmap_bf16(&tm_a, A, static_cast<uint64_t>(n_adapters * r), static_cast<uint64_t>(in),
                       static_cast<uint32_t>(r8)))
     return QLORA_ERR_CUDA;
-  if (tiles * a.groups > kMaxTokens) return QLORA_ERR_UNSUPPORTED_SHAPE;
   const int smem = qnf4::uu_smem_bytes(a.N);
   QLORA_CUDA_TRY(set_max_smem(reinterpret_cast<const void*>(qnf4::slots_us_umma_kernel), smem));
   cudaLaunchConfig_t cfg{};
@@ -1835,7 +1836,9 @@ int qlora_linear_fwd_slots(const uint16_t* x, int64_t M, const qlora_nf4_weight*
     return QLORA_ERR_INVALID_ARG;
   const int sc = check_linear_shapes(M, w, r);
   if (sc != QLORA_OK) return sc;
-  if (n_adapters < 1 || n_adapters * r > kMaxTokens) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (n_adapters < 1 || n_adapters > kMaxTokens / r) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  // the rank-r launch has at most 128 groups of adapters per 128 tokens
+  if (M > 256 && cdiv(M, 128) * std::min<int64_t>(n_adapters, 128) > kMaxTokens) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < slots_ws(M, w->cols, w->rows, r).total)
     return QLORA_ERR_WORKSPACE;
   return linear_fwd_slots_impl(x, M, w, A, B, n_adapters, r, scale, ids, h, workspace,

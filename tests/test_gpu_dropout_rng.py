@@ -256,3 +256,50 @@ def test_python_refusals(cuda_lib):
     with pytest.raises(ValueError):
         q.linear_bwd_dropout_rng(dh, x, us[:4], w, A, B, 8.0, rng, 0.1)
     assert qmod.dropout_keep_bits(rng, 0.1, 0, 64).numel() == 0
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Forward and backward calls of different shapes on two streams at a time."""
+    q = cuda_lib
+    cases = []
+    for M, r in ((40, 16), (300, 88), (1100, 64), (200, 8)):
+        prob = synth.problem(M, 512, 384, r, seed=M)
+        w = q.quantize_nf4(prob["W"].cuda())
+        x, A, B, dh = (prob[k].cuda() for k in ("x", "A", "B", "dh"))
+        rng = rng_tensor(M, 1)
+
+        def step(x=x, w=w, A=A, B=B, dh=dh, rng=rng):
+            h, us = q.linear_fwd_dropout_rng(x, w, A, B, 32.0, rng, 0.1)
+            return (h, us) + q.linear_bwd_dropout_rng(dh, x, us, w, A, B, 32.0, rng, 0.1)
+        cases.append((step, step()))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for k in range(8):
+        for st, j in ((s1, k % 4), (s2, (k + 2) % 4)):
+            with torch.cuda.stream(st):
+                got.append((cases[j][0](), cases[j][1]))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    assert q.last_device_status() == 0
+
+
+def test_infinities_in_dropped_places_change_nothing(cuda_lib):
+    """The adapter branch never sees a dropped value, whatever it is: us, dA
+    and dB stay as they are (the base product of h and dx does see x, dh)."""
+    q = cuda_lib
+    for M in (12, 300):
+        prob = synth.problem(M, 256, 192, 16, seed=M)
+        w = q.quantize_nf4(prob["W"].cuda())
+        x, A, B, dh = (prob[k].cuda() for k in ("x", "A", "B", "dh"))
+        rng = rng_tensor(5, M)
+        bits = q.dropout_keep_bits(rng, 0.3, M, 256).cpu().numpy()
+        drop = torch.from_numpy(linear.unpack_keep(bits, 256) == 0).cuda()
+        _, us = q.linear_fwd_dropout_rng(x, w, A, B, 32.0, rng, 0.3)
+        _, dA, dB = q.linear_bwd_dropout_rng(dh, x, us, w, A, B, 32.0, rng, 0.3)
+        bad = torch.where(drop, torch.full_like(x, float("inf")), x)
+        bad[0, drop[0].nonzero()[0]] = float("nan")
+        _, us1 = q.linear_fwd_dropout_rng(bad, w, A, B, 32.0, rng, 0.3)
+        _, dA1, dB1 = q.linear_bwd_dropout_rng(dh, bad, us1, w, A, B, 32.0, rng, 0.3)
+        assert torch.equal(us, us1) and torch.equal(dA, dA1) and torch.equal(dB, dB1)

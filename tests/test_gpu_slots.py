@@ -233,3 +233,40 @@ def test_a_broken_adapter_reaches_its_own_tokens_only(cuda_lib, M):
     touched[[7, 130]] = True
     assert torch.equal(h0[mine][:, ~touched], h1[mine][:, ~touched])
     assert bool(h1[mine][:, 7].isnan().all()) and not bool(h1[mine][:, 130].isfinite().any())
+
+
+def test_two_calls_at_once_and_graphs_that_share_a_workspace(cuda_lib):
+    """Calls on two streams at a time, and two captured graphs over one
+    workspace replayed in turn, give what single calls give."""
+    q = cuda_lib
+    cases = []
+    for M, r, n in ((24, 16, 20), (200, 24, 3), (230, 16, 100), (600, 64, 6)):
+        W, x, A, B, scale = (t.cuda() for t in make(M, 768, 640, r, n, seed=M))
+        ids = torch.from_numpy(mixed(M, n, M).astype(np.int32)).cuda()
+        args = (x, q.quantize_nf4(W), A, B, scale, ids)
+        cases.append((args, q.linear_fwd_slots(*args)))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for k in range(12):
+        for st, (args, _) in ((s1, cases[k % 4]), (s2, cases[(k + 1) % 4])):
+            with torch.cuda.stream(st):
+                got.append(q.linear_fwd_slots(*args))
+    torch.cuda.synchronize()
+    want = [c for k in range(12) for c in (cases[k % 4][1], cases[(k + 1) % 4][1])]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for args, h in cases[:3]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = q.linear_fwd_slots(*args, workspace=ws)
+        graphs.append((g, out, h))
+    for _ in range(3):
+        for g, out, h in graphs:
+            out.zero_()
+            ws.fill_(0xFF)                  # what the workspace holds before does not matter
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, h)
+    assert q.last_device_status() == 0
