@@ -17,6 +17,7 @@ FAKE = 1 << 20
 def lib():
     from bit_nf4_quantized_11_b200 import build
     build.build()
+    q._LIB = None          # bind anew: a test that reloads the module leaves the old module's types in the library
     return q.load()
 
 
