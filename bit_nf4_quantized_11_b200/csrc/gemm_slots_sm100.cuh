@@ -33,7 +33,11 @@
 // for a 64 KB table instead, for every byte of two codes the two fp32 levels,
 // one copy per lane: a pair of weights takes one prmt (the address), one
 // 8-byte shared load, one packed fp32 multiply and one conversion, and every
-// weight is bf16(level * scale) as everywhere else.
+// weight is bf16(level * scale) as everywhere else.  Under that load every
+// shared-memory access (a barrier poll too) takes about 300 clocks, so the
+// chain of a block counts: its lookups go out in four batches of 8, the next
+// one before the last is converted, and the barriers ahead are polled before
+// the last batches and looked at behind them.
 //
 // Roles per CTA (24 warps):
 //   warp 0        TMA of the x tiles (one copy per stage)
@@ -119,6 +123,22 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint32_t bar, uint32_t parity
       : "=r"(ok) : "r"(bar), "r"(parity), "r"(20000u) : "memory");
   return ok != 0;
 }
+// The waiting part of a bounded wait, out of line: two dozen copies of it cost
+// instruction fetches in the roles' loops.
+__device__ __noinline__ bool sg_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag) {
+  if (mbar_try_wait_hint(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait_hint(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > timeout_ns) {
+      *abort_flag = 1;
+      raise_device_error(1);
+      return false;
+    }
+  }
+  return true;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem desc]^T, bf16 inputs, fp32 accumulate; the
 // descriptor's halves apart, since only the low one changes along K.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
@@ -155,6 +175,25 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+// 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Whether a phase is complete, without waiting: asked early, looked at late.
+__device__ __forceinline__ uint32_t mbar_probe(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok;
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -279,18 +318,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
 
   // Bounded wait; false once it, or any other wait of the CTA, ran out of time.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    const uint32_t a = smem_u32(bar);
-    if (mbar_try_wait_hint(a, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait_hint(a, parity)) {
-      if (*abort_flag) return false;
-      if (global_timer_ns() - t0 > tmo) {
-        *abort_flag = 1;
-        raise_device_error(1);
-        return false;
-      }
-    }
-    return true;
+    return mbar_probe(bar, parity) != 0 || sg_wait(smem_u32(bar), parity, tmo, abort_flag);
   };
   // the same answer for every lane of a warp (the roles that work as whole warps)
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
@@ -467,8 +495,11 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
     // block before it completes.
     uint32_t c[8];
     float c_hat = 0.f;
-    auto read_codes = [&]() {
-      if (!wait_warp(sfull + cs, cph)) return false;
+    auto settled = [&](uint32_t probed, uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu, probed) != 0 || wait_warp(bar, parity);
+    };
+    auto read_codes = [&](uint32_t probed) {
+      if (!settled(probed, sfull + cs, cph)) return false;
       const uint32_t crow = smem_u32(c_ring + cs * kSgCodeTile) + t * 128;
       lds_v4(crow + (((2 * g) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[0]));
       lds_v4(crow + (((2 * g + 1) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[4]));
@@ -479,29 +510,50 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       return true;
     };
     bool ok = true;
-    if (uu < UB) ok = read_codes();
+    if (uu < UB) ok = read_codes(0);
     for (int i = 0; i < n_u && ok; ++i) {
       const int it = i * SPU + g / KB, sa = it % SA;
-      uint32_t v[32];
-      if (uu < UB) {
-        if (kLut) {
-          uint64_t c2;
-          asm("mov.b64 %0, {%1, %1};" : "=l"(c2) : "f"(c_hat));
+      const bool more = i + 1 < n_u && (uu + 1 == UPT || uu + 1 < UB);    // a base unit follows
+      const uint32_t a_blk = a_lane + (sa * KB + ib) * 32, a_par = ((it / SA) & 1u) ^ 1u;
+      uint32_t next = 0;                                     // its codes are there
+      if (kLut && uu < UB) {
+        const uint32_t free = mbar_probe(aempty + sa, a_par);
+        uint64_t c2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(c2) : "f"(c_hat));
+        uint64_t lv[4][8];
+        uint32_t w[16];
+        auto lookup = [&](int q) {                           // the 8 bytes of codes 2 q, 2 q + 1
 #pragma unroll
-          for (int w = 0; w < 8; ++w) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              // bytes of the address: {lane copy, code byte, table, 0}
-              const uint32_t addr = prmt(lut_base, c[w], 0x3200u | ((4u + b) << 4));
-              uint64_t lv;
-              asm volatile("ld.shared.b64 %0, [%1];" : "=l"(lv) : "r"(addr));
-              asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(lv) : "l"(c2));
-              float lo, hi2;
-              asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi2) : "l"(lv));
-              v[4 * w + b] = pack_bf16x2_rn(lo, hi2);
-            }
+          for (int b = 0; b < 8; ++b) {
+            // bytes of the address: {lane copy, code byte, table, 0}
+            const uint32_t addr = prmt(lut_base, c[2 * q + (b >> 2)], 0x3200u | ((4u + (b & 3)) << 4));
+            asm volatile("ld.shared.b64 %0, [%1];" : "=l"(lv[q][b]) : "r"(addr));
           }
-        } else {
+        };
+        auto convert = [&](int q) {
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(lv[q][b]) : "l"(c2));
+            float lo, hi2;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi2) : "l"(lv[q][b]));
+            w[8 * (q & 1) + b] = pack_bf16x2_rn(lo, hi2);
+          }
+        };
+        lookup(0);
+        lookup(1);
+        convert(0);
+        lookup(2);
+        convert(1);
+        if (!(ok = settled(free, aempty + sa, a_par))) break;
+        tmem_st_32x32b_x16(a_blk, w);
+        if (more) next = mbar_probe(sfull + cs, cph);
+        lookup(3);
+        convert(2);
+        convert(3);
+        tmem_st_32x32b_x16(a_blk + 16, w);
+      } else if (uu < UB) {
+        uint32_t v[32];
+        {
           const Nf4Table tb = make_table(args.L, c_hat);
 #pragma unroll
           for (int w = 0; w < 8; ++w) {
@@ -510,8 +562,10 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
             v[4 * w] = o[0]; v[4 * w + 1] = o[1]; v[4 * w + 2] = o[2]; v[4 * w + 3] = o[3];
           }
         }
-        if (!(ok = wait_warp(aempty + sa, ((it / SA) & 1u) ^ 1u))) break;
+        if (!(ok = wait_warp(aempty + sa, a_par))) break;
+        tmem_st_32x32b_x32(a_blk, v);
       } else {
+        uint32_t v[32];
         // adapter block: rank columns [64 e, 64 e + 64) of the listed adapters, in chunks of 8
         const int e = (uu - UB) * 4 + g;
         const int row = tile * kSgRows + t;
@@ -536,7 +590,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
           j0 += 8;
           if (j0 == args.r8) { j0 = 0; ++li; }
         }
-        if (!(ok = wait_warp(aempty + sa, ((it / SA) & 1u) ^ 1u))) break;
+        if (!(ok = wait_warp(aempty + sa, a_par))) break;
         if (SA > S && !(ok = x_done(it))) break;
         grid_dependency_wait();                              // us comes from the kernel before
         // the tokens' us under the columns of their own adapter, zero elsewhere
@@ -565,9 +619,9 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
             if ((v[w] & 0x7F800000u) == 0x7F800000u) v[w] &= 0xFFFFu;
           }
         }
+        tmem_st_32x32b_x32(a_blk, v);
       }
-      tmem_st_32x32b_x32(a_lane + (sa * KB + ib) * 32, v);
-      if (i + 1 < n_u && (uu + 1 == UPT || uu + 1 < UB) && !(ok = read_codes())) break;
+      if (more && !(ok = read_codes(next))) break;
       tmem_st_wait();
       tc_fence_before_sync();
       __syncwarp();
