@@ -670,8 +670,8 @@ def selftest_wait_timeout() -> int:
 
 KERNEL_NAMES = ("quantize_blocks", "scale_mean_tree", "dq_scales", "dequantize", "gemm_fwd", "gemm_dx",
                 "gemv", "gemv_finalize", "lora_rowwise", "lora_rowwise_du", "lora_colwise",
-                "merge_adapter", "dropout_dx", "lora_fewtok", "lora_pad", "token_slots", "slots_tiles", "slots_us", "slots_gemm",
-                "keep_bits")
+                "merge_adapter", "dropout_dx", "lora_fewtok", "lora_pad", "token_slots", "slots_tiles", "slots_us",
+                "slots_gemm", "keep_bits")
 
 
 def timing_enable(on: bool = True) -> bool:

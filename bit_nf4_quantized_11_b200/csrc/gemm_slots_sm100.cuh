@@ -43,6 +43,7 @@
 //   warp 0        TMA of the x tiles (one copy per stage)
 //   warp 1        TMEM allocation; UMMA issue
 //   warp 2        TMA of the code tiles (128 rows x 128 bytes: one unit)
+//   warp 3        waits for the kernel before, so that no CTA ends ahead of it
 //   warps 4-7     block scales of each code tile (one row per thread)
 //   warps 8-23    four dequant groups of 4 warps, group g takes the g-th
 //                 64-wide block of every unit; then the epilogue
@@ -407,6 +408,10 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       for (int k = issued > kSgUnits ? issued - kSgUnits : 0; k < issued; ++k)
         mbar_wait_bounded(cfull + (k % kSgUnits), (k / kSgUnits) & 1u, tmo);
     }
+  } else if (warp == 3) {
+    // With no adapter in use and no tile cut nothing else waits for the kernel
+    // before; what follows this one in the stream relies on it too.
+    grid_dependency_wait();
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ block scales
     // Thread t owns row t of each tile: the four scales of each code tile,

@@ -506,8 +506,9 @@ int qlora_selftest_wait_timeout(void* stream);
  * "scale_mean_tree", "dq_scales", "dequantize", "gemm_fwd", "gemm_dx",
  * "gemv", "gemv_finalize", "lora_rowwise" (us), "lora_rowwise_du" (du),
  * "lora_colwise" (dA and dB), "merge_adapter", "dropout_dx", "token_slots",
- * "slots_tiles", "slots_us", "slots_gemm", "keep_bits".  Events are created by the library on first use (host-side
- * CUDA objects, no device memory).  Not for use during stream capture.
+ * "slots_tiles", "slots_us", "slots_gemm", "keep_bits".  Events are created
+ * by the library on first use (host-side CUDA objects, no device memory).
+ * Not for use during stream capture.
  *
  * qlora_timing_enable: on != 0 enables, 0 disables; returns the previous state.
  * qlora_timing_reset: forgets all recorded launches.
