@@ -54,6 +54,8 @@
 // Every wait is bounded, as in gemm_sm100.cuh; no TMA multicast.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "slots.cuh"
 
@@ -214,8 +216,20 @@ __device__ __forceinline__ void lds_v4(uint32_t addr, uint32_t (&v)[4]) {
 
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// First unit of CTA c when T units are dealt out to G CTAs.
-__device__ __forceinline__ int64_t sg_unit_begin(int64_t c, int64_t T, int64_t G) { return T * c / G; }
+// T units dealt out to G CTAs: CTA c begins at floor(T c / G).  (T fits 32 bits:
+// at most 2^23 row tiles with 256 adapter units each, and 2^40 weights.)
+struct SgDeal {
+  uint32_t T, G, each, rest;
+  __device__ SgDeal(uint32_t T_, uint32_t G_) : T(T_), G(G_), each(T_ / G_), rest(T_ % G_) {}
+  __device__ __forceinline__ uint32_t begin(uint32_t c) const { return each * c + rest * c / G; }
+  // the CTA that holds unit u
+  __device__ __forceinline__ int holder(uint32_t u) const {
+    int c = min(static_cast<int>(G) - 1, static_cast<int>(static_cast<float>(u) * (static_cast<float>(G) / static_cast<float>(T))));
+    while (c > 0 && begin(c) > u) --c;
+    while (c + 1 < static_cast<int>(G) && begin(c + 1) <= u) ++c;
+    return c;
+  }
+};
 
 // KB, kLut: sg_kb(N), sg_lut(N).
 template <int KB, bool kLut>
@@ -261,6 +275,11 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   const int n_blk = args.K / 64;
   const int UB = (n_blk + 3) / 4;                            // base units per tile
 
+  // The tokens' slots (-1: no adapter, or past the batch): of up to 32 tokens
+  // every warp looks at all, of more each thread has its own.
+  const bool one_warp = args.M <= 32;
+  int32_t my_id = -1;
+  if (one_warp && lane < args.M) my_id = args.ids != nullptr ? __ldg(args.ids + lane) : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSgMaxStages; ++s) {
       mbar_init(xfull + s, 1);
@@ -286,35 +305,35 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
     tmem_alloc(tmem_holder, kSgTmemCols);
     tmem_relinquish();
   }
-  // The tokens' slots (-1: no adapter, or past the batch) and the distinct
-  // ones; the hash table lies over the code ring, which is not in use yet.
-  int32_t my_id = -1;
-  if (threadIdx.x < kSgMaxN && static_cast<int>(threadIdx.x) < args.M) {
+  if (!one_warp && threadIdx.x < kSgMaxN && static_cast<int>(threadIdx.x) < args.M)
     my_id = args.ids != nullptr ? __ldg(args.ids + threadIdx.x) : 0;
-    if (my_id < 0 || my_id >= args.n_adapters) my_id = -1;
-  }
-  if (kLut) {
-    // row b (256 bytes): lane l's copy of {level of the low code, level of the high code} at 8 l
-    for (int b = warp; b < 256; b += kSgThreads / 32)
-      *reinterpret_cast<float2*>(table + b * 256 + lane * 8) = make_float2(args.L.v[b & 15], args.L.v[b >> 4]);
+  if (my_id < 0 || my_id >= args.n_adapters) my_id = -1;
+  int n_list, place;
+  if (one_warp) {                                            // every warp for itself
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, my_id);
+    const int first = __ffs(static_cast<int>(same)) - 1;
+    const uint32_t lead = __ballot_sync(0xFFFFFFFFu, my_id >= 0 && first == lane);
+    n_list = __popc(lead);
+    place = my_id < 0 ? -1 : __popc(lead & ((1u << first) - 1u));
+    if (warp == 3) {
+      if (my_id >= 0 && first == lane) list[place] = my_id;
+      tok_col[lane] = place < 0 ? -(1 << 29) : place * args.r8;
+    }
+  } else {                                                   // the hash table lies over the code ring, not in use yet
+    n_list = distinct_slots<kSgMaxN, kSgHash>(my_id, reinterpret_cast<int32_t*>(c_ring), list, counts, place);
+    if (threadIdx.x < kSgMaxN) tok_col[threadIdx.x] = place < 0 ? -(1 << 29) : place * args.r8;
+    fence_proxy_async_smem();                                // the table's words before the copies over them
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  int place;
-  const int n_list =
-      distinct_slots<kSgMaxN, kSgHash>(my_id, reinterpret_cast<int32_t*>(c_ring), list, counts, place);
-  if (threadIdx.x < kSgMaxN) tok_col[threadIdx.x] = place < 0 ? -(1 << 29) : place * args.r8;
-  fence_proxy_async_smem();                                  // the table's words before the copies over them
-  __syncthreads();
   const uint32_t tmem_base = *tmem_holder;
   const int k_low = n_list * args.r8;                        // rank columns of the listed adapters
   const int low_blk = (k_low + 63) / 64;
   const int UPT = UB + (low_blk + 3) / 4;                    // units per tile
-  const int64_t G = gridDim.x;
-  const int64_t T = static_cast<int64_t>((args.out + kSgRows - 1) / kSgRows) * UPT;
-  const int64_t g0 = sg_unit_begin(blockIdx.x, T, G);
-  const int n_u = static_cast<int>(sg_unit_begin(blockIdx.x + 1, T, G) - g0);   // this CTA's units
+  const SgDeal deal(static_cast<uint32_t>((args.out + kSgRows - 1) / kSgRows) * UPT, gridDim.x);
+  const uint32_t g0 = deal.begin(blockIdx.x);
+  const int n_u = static_cast<int>(deal.begin(blockIdx.x + 1) - g0);           // this CTA's units
   const int tile0 = static_cast<int>(g0 / UPT), uu0 = static_cast<int>(g0 % UPT);
 
   // Bounded wait; false once it, or any other wait of the CTA, ran out of time.
@@ -485,6 +504,15 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       return slots_odd_term(args.B + (a * args.out + n) * args.r,
                                           args.us + static_cast<int64_t>(m) * args.r8, args.r);
     };
+    if (kLut) {
+      // row b (256 bytes): lane l's copy of {level of the low code, level of the high code} at 8 l
+      const float low_level = args.L.v[warp - 8];
+      static_assert(kSgDecThreads == 512, "a warp fills the rows of one low code");
+#pragma unroll
+      for (int hi = 0; hi < 16; ++hi)
+        *reinterpret_cast<float2*>(table + (16 * hi + warp - 8) * 256 + lane * 8) = make_float2(low_level, args.L.v[hi]);
+      asm volatile("bar.sync 1, 512;" ::: "memory");
+    }
     uint32_t dph = 0;
     auto dec_sync = [&]() {                                  // all dequant warps, bounded
       __syncwarp();
@@ -685,17 +713,13 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       const int tl = c == 0 ? cut_first : cut_last;
       if (tl < 0) continue;
       // CTAs that hold units of this tile, in order: c_first .. c_last
-      const int64_t u_lo = static_cast<int64_t>(tl) * UPT, u_hi = u_lo + UPT;
-      int c_first = static_cast<int>(u_lo * G / T), c_last = static_cast<int>((u_hi - 1) * G / T);
-      while (c_first + 1 < G && sg_unit_begin(c_first + 1, T, G) <= u_lo) ++c_first;
-      while (c_first > 0 && sg_unit_begin(c_first, T, G) > u_lo) --c_first;
-      while (c_last + 1 < G && sg_unit_begin(c_last + 1, T, G) < u_hi) ++c_last;
-      while (c_last > 0 && sg_unit_begin(c_last, T, G) >= u_hi) --c_last;
+      const int c_first = deal.holder(static_cast<uint32_t>(tl) * UPT);
+      const int c_last = deal.holder(static_cast<uint32_t>(tl) * UPT + UPT - 1);
       const int n_parts = c_last - c_first + 1;
       // where each of them left its part: its first tile's, or its last one's
       if (static_cast<int>(threadIdx.x) - 256 < n_parts) {
         const int k = c_first + static_cast<int>(threadIdx.x) - 256;
-        parts[threadIdx.x - 256] = 2 * k + (sg_unit_begin(k, T, G) / UPT == tl ? 0 : 1);
+        parts[threadIdx.x - 256] = 2 * k + (deal.begin(k) / UPT == static_cast<uint32_t>(tl) ? 0 : 1);
       }
       if (!(ok = dec_sync())) break;
       const uint32_t old = static_cast<uint32_t>(last_flag[2 * c]);
@@ -703,45 +727,51 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
         __threadfence();
         const bool any_odd = (old >> 16) != 0 || last_flag[2 * c + 1] != 0;
         const int n = tl * kSgRows + 4 * lane;
-        // one warp per four tokens, four rows per lane; the parts of two CTAs
-        // are under way together, added in CTA order
-        for (int m0 = (warp - 8) * 4; m0 < args.M; m0 += kSgDecThreads / 32 * 4) {
-          float4 d[4];
+        // A warp's tokens, four rows per lane; the loads of 8 values under way
+        // together: of up to 16 tokens one per warp and 8 parts, of more four
+        // tokens and two parts.  Added in CTA order.
+        auto add_up = [&](auto tokens) {
+          constexpr int kTok = decltype(tokens)::value, kPart = 8 / kTok;
+          for (int m0 = (warp - 8) * kTok; m0 < args.M; m0 += kSgDecThreads / 32 * kTok) {
+            float4 d[kTok];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) d[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p0 = 0; p0 < n_parts; p0 += 2) {
-            float4 p[2][4];
+            for (int k = 0; k < kTok; ++k) d[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p0 = 0; p0 < n_parts; p0 += kPart) {
+              float4 p[kPart][kTok];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float* src = args.part + (static_cast<int64_t>(parts[min(p0 + j, n_parts - 1)]) * N + m0) * kSgRows +
-                                 4 * lane;
+              for (int j = 0; j < kPart; ++j) {
+                if (p0 + j >= n_parts) break;
+                const float* src = args.part + (static_cast<int64_t>(parts[p0 + j]) * N + m0) * kSgRows + 4 * lane;
 #pragma unroll
-              for (int k = 0; k < 4; ++k)                    // (rows up to N, a multiple of 16, are there)
-                p[j][k] = __ldcg(reinterpret_cast<const float4*>(src + k * kSgRows));
-            }
+                for (int k = 0; k < kTok; ++k)               // (rows up to N, a multiple of 16, are there)
+                  p[j][k] = __ldcg(reinterpret_cast<const float4*>(src + k * kSgRows));
+              }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (p0 + j >= n_parts) break;
+              for (int j = 0; j < kPart; ++j) {
+                if (p0 + j >= n_parts) break;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                d[k].x += p[j][k].x; d[k].y += p[j][k].y; d[k].z += p[j][k].z; d[k].w += p[j][k].w;
+                for (int k = 0; k < kTok; ++k) {
+                  d[k].x += p[j][k].x; d[k].y += p[j][k].y; d[k].z += p[j][k].z; d[k].w += p[j][k].w;
+                }
               }
             }
-          }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int m = m0 + k;
-            if (m >= args.M || n >= args.out) break;
-            if (any_odd) {
-              d[k].x += odd_term(m, n);
-              d[k].y += odd_term(m, n + 1);
-              d[k].z += odd_term(m, n + 2);
-              d[k].w += odd_term(m, n + 3);
+            for (int k = 0; k < kTok; ++k) {
+              const int m = m0 + k;
+              if (m >= args.M || n >= args.out) break;
+              if (any_odd) {
+                d[k].x += odd_term(m, n);
+                d[k].y += odd_term(m, n + 1);
+                d[k].z += odd_term(m, n + 2);
+                d[k].w += odd_term(m, n + 3);
+              }
+              *reinterpret_cast<uint2*>(args.h + static_cast<int64_t>(m) * args.out + n) =
+                  make_uint2(pack_bf16x2_rn(d[k].x, d[k].y), pack_bf16x2_rn(d[k].z, d[k].w));
             }
-            *reinterpret_cast<uint2*>(args.h + static_cast<int64_t>(m) * args.out + n) =
-                make_uint2(pack_bf16x2_rn(d[k].x, d[k].y), pack_bf16x2_rn(d[k].z, d[k].w));
           }
-        }
+        };
+        if (args.M <= 16) add_up(std::integral_constant<int, 1>{});
+        else add_up(std::integral_constant<int, 4>{});
       }
       if (!(ok = dec_sync())) break;                         // parts are read
     }
