@@ -84,7 +84,7 @@ __host__ __device__ constexpr bool sg_lut(int N) { return N <= 128; }
 // and barriers before it.  Without the table x starts at the boundary.
 constexpr uint32_t kSgTableAt = 0x10000;
 __host__ __device__ constexpr int sg_low_bytes() {
-  return kSgUnits * (kSgCodeTile + kSgRows * 16) + 2 * kSgMaxN * 4 + kSgMaxCtas * 4 + 64 + 512;
+  return kSgUnits * (kSgCodeTile + kSgRows * 16) + 2 * kSgMaxN * 4 + 64 + 512;
 }
 // No other CTA of this library that allocates tensor memory fits beside this
 // one (the rank-r kernels take 72 KB or more): two that waited for each
@@ -251,10 +251,10 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   int32_t* list = reinterpret_cast<int32_t*>(s_ring + kSgUnits * kSgRows * 4);
                                                                                     // distinct adapters, first appearance first
   int32_t* tok_col = list + kSgMaxN;                         // a token's first rank column, or far past the last
-  int32_t* parts = tok_col + kSgMaxN;                        // the partials of the tile being added up
-  int32_t* counts = parts + kSgMaxCtas;                      // [8] leaders per warp of 32 tokens
+  int32_t* counts = tok_col + kSgMaxN;                       // [8] leaders per warp of 32 tokens
   volatile int32_t* odd = counts + 8;                        // [2] by segment: a B value was not finite
-  volatile int32_t* last_flag = counts + 10;                 // [2 segments][2]: this CTA adds the tile up; some part was odd
+  volatile int32_t* last_flag = counts + 10;                 // [2]: the ticket of the CTA's first and last tile
+  volatile int32_t* cut = counts + 12;                       // [2][2]: their first CTA's partial, how many CTAs share them
   uint8_t* x_ring = kLut ? table + 65536 : table;
   uint64_t* bars = reinterpret_cast<uint64_t*>(counts + 16);
   uint64_t* xfull = bars;                                    // the stage's x tile landed
@@ -304,6 +304,14 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
   if (warp == 1) {
     tmem_alloc(tmem_holder, kSgTmemCols);
     tmem_relinquish();
+  }
+  if (kLut && warp >= 8) {
+    // row b (256 bytes): lane l's copy of {level of the low code, level of the high code} at 8 l
+    const float low_level = args.L.v[warp - 8];
+    static_assert(kSgDecThreads == 512, "a warp fills the rows of one low code");
+#pragma unroll
+    for (int hi = 0; hi < 16; ++hi)
+      *reinterpret_cast<float2*>(table + (16 * hi + warp - 8) * 256 + lane * 8) = make_float2(low_level, args.L.v[hi]);
   }
   if (!one_warp && threadIdx.x < kSgMaxN && static_cast<int>(threadIdx.x) < args.M)
     my_id = args.ids != nullptr ? __ldg(args.ids + threadIdx.x) : 0;
@@ -504,15 +512,6 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       return slots_odd_term(args.B + (a * args.out + n) * args.r,
                                           args.us + static_cast<int64_t>(m) * args.r8, args.r);
     };
-    if (kLut) {
-      // row b (256 bytes): lane l's copy of {level of the low code, level of the high code} at 8 l
-      const float low_level = args.L.v[warp - 8];
-      static_assert(kSgDecThreads == 512, "a warp fills the rows of one low code");
-#pragma unroll
-      for (int hi = 0; hi < 16; ++hi)
-        *reinterpret_cast<float2*>(table + (16 * hi + warp - 8) * 256 + lane * 8) = make_float2(low_level, args.L.v[hi]);
-      asm volatile("bar.sync 1, 512;" ::: "memory");
-    }
     uint32_t dph = 0;
     auto dec_sync = [&]() {                                  // all dequant warps, bounded
       __syncwarp();
@@ -523,7 +522,17 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
     };
     int uu = uu0, tile = tile0, seg = 0, cs = 0, seg_uu = uu0;
     uint32_t cph = 0;
-    int cut_first = -1, cut_last = -1;                       // this CTA's cut tiles
+    // The CTA's first and last tile, cut between CTAs or not: which CTAs hold
+    // units of them.  Found here, while the first codes are on their way.
+    if (threadIdx.x < 256 + 2) {
+      const int c = static_cast<int>(threadIdx.x) - 256;
+      const uint32_t u_lo = (c == 0 ? static_cast<uint32_t>(tile0) : (g0 + n_u - 1) / UPT) * UPT;
+      const int c_first = deal.holder(u_lo);
+      // (a CTA leaves the part of its first tile in its first partial, that of its last one in its second)
+      cut[2 * c] = 2 * c_first + (deal.begin(c_first) < u_lo ? 1 : 0);
+      cut[2 * c + 1] = deal.holder(u_lo + UPT - 1) - c_first + 1;
+      last_flag[c] = -1;
+    }
     // The codes and the scale of a unit's block are read while the store of the
     // block before it completes.
     uint32_t c[8];
@@ -694,13 +703,10 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       if (!whole) {
         // the answer is read when this CTA is done with its units: the part
         // that ends here is rarely the tile's last
-        const int c = seg > 0 ? 1 : 0;
-        if (seg > 0) cut_last = tile;
-        else cut_first = tile;
         if (threadIdx.x == 256) {
           grid_dependency_wait();                            // the kernel before zeroes the tickets
-          last_flag[2 * c] = static_cast<int32_t>(atomicAdd(args.tickets + tile, 1u | (my_odd ? 0x10000u : 0u)));
-          last_flag[2 * c + 1] = my_odd;
+          const uint32_t mine = 1u | (my_odd ? 0x10000u : 0u);
+          last_flag[seg > 0 ? 1 : 0] = static_cast<int32_t>(atomicAdd(args.tickets + tile, mine) + mine);
         }
       }
       ++seg;
@@ -708,72 +714,67 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       if (uu == UPT) { uu = 0; ++tile; }
     }
     // ------------------------------------------------------------ tiles cut between CTAs
-#pragma unroll 1
-    for (int c = 0; c < 2 && ok; ++c) {
-      const int tl = c == 0 ? cut_first : cut_last;
-      if (tl < 0) continue;
-      // CTAs that hold units of this tile, in order: c_first .. c_last
-      const int c_first = deal.holder(static_cast<uint32_t>(tl) * UPT);
-      const int c_last = deal.holder(static_cast<uint32_t>(tl) * UPT + UPT - 1);
-      const int n_parts = c_last - c_first + 1;
-      // where each of them left its part: its first tile's, or its last one's
-      if (static_cast<int>(threadIdx.x) - 256 < n_parts) {
-        const int k = c_first + static_cast<int>(threadIdx.x) - 256;
-        parts[threadIdx.x - 256] = 2 * k + (deal.begin(k) / UPT == static_cast<uint32_t>(tl) ? 0 : 1);
-      }
-      if (!(ok = dec_sync())) break;
-      const uint32_t old = static_cast<uint32_t>(last_flag[2 * c]);
-      if ((old & 0xFFFFu) == static_cast<uint32_t>(n_parts - 1)) {
-        __threadfence();
-        const bool any_odd = (old >> 16) != 0 || last_flag[2 * c + 1] != 0;
-        const int n = tl * kSgRows + 4 * lane;
-        // A warp's tokens, four rows per lane; the loads of 8 values under way
-        // together: of up to 16 tokens one per warp and 8 parts, of more four
-        // tokens and two parts.  Added in CTA order.
-        auto add_up = [&](auto tokens) {
-          constexpr int kTok = decltype(tokens)::value, kPart = 8 / kTok;
-          for (int m0 = (warp - 8) * kTok; m0 < args.M; m0 += kSgDecThreads / 32 * kTok) {
-            float4 d[kTok];
+    if (ok) ok = dec_sync();                                 // the tickets are there
+    int32_t ticket[2];
 #pragma unroll
-            for (int k = 0; k < kTok; ++k) d[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p0 = 0; p0 < n_parts; p0 += kPart) {
-              float4 p[kPart][kTok];
+    for (int c = 0; c < 2; ++c) {
+      ticket[c] = last_flag[c];
+      if (!ok || ticket[c] < 0 || (ticket[c] & 0xFFFF) != cut[2 * c + 1]) ticket[c] = 0;    // not the last to finish
+    }
+    if ((ticket[0] | ticket[1]) != 0) {
+      __threadfence();
+      // Four rows per lane; the loads of 8 values under way together: of up to
+      // 16 tokens one per warp and 8 parts, of more four tokens and two parts.
+      // Added in CTA order.
+      auto add_up = [&](auto tokens) {
+        constexpr int kTok = decltype(tokens)::value, kPart = 8 / kTok;
+        const int steps = (args.M + kTok - 1) / kTok;
+        for (int e = warp - 8; e < 2 * steps; e += kSgDecThreads / 32) {
+          const int c = e < steps ? 0 : 1, m0 = (e - c * steps) * kTok;
+          if (ticket[c] == 0) continue;
+          const int tl = c == 0 ? tile0 : static_cast<int>((g0 + n_u - 1) / UPT);
+          const int n = tl * kSgRows + 4 * lane, p_first = cut[2 * c], n_parts = cut[2 * c + 1];
+          float4 d[kTok];
 #pragma unroll
-              for (int j = 0; j < kPart; ++j) {
-                if (p0 + j >= n_parts) break;
-                const float* src = args.part + (static_cast<int64_t>(parts[p0 + j]) * N + m0) * kSgRows + 4 * lane;
+          for (int k = 0; k < kTok; ++k) d[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int p0 = 0; p0 < n_parts; p0 += kPart) {
+            float4 p[kPart][kTok];
 #pragma unroll
-                for (int k = 0; k < kTok; ++k)               // (rows up to N, a multiple of 16, are there)
-                  p[j][k] = __ldcg(reinterpret_cast<const float4*>(src + k * kSgRows));
-              }
+            for (int j = 0; j < kPart; ++j) {
+              if (p0 + j >= n_parts) break;
+              // the CTAs behind the first begin within the tile: their first partial
+              const int at = p0 + j == 0 ? p_first : (p_first & ~1) + 2 * (p0 + j);
+              const float* src = args.part + (static_cast<int64_t>(at) * N + m0) * kSgRows + 4 * lane;
 #pragma unroll
-              for (int j = 0; j < kPart; ++j) {
-                if (p0 + j >= n_parts) break;
-#pragma unroll
-                for (int k = 0; k < kTok; ++k) {
-                  d[k].x += p[j][k].x; d[k].y += p[j][k].y; d[k].z += p[j][k].z; d[k].w += p[j][k].w;
-                }
-              }
+              for (int k = 0; k < kTok; ++k)                 // (rows up to N, a multiple of 16, are there)
+                p[j][k] = __ldcg(reinterpret_cast<const float4*>(src + k * kSgRows));
             }
 #pragma unroll
-            for (int k = 0; k < kTok; ++k) {
-              const int m = m0 + k;
-              if (m >= args.M || n >= args.out) break;
-              if (any_odd) {
-                d[k].x += odd_term(m, n);
-                d[k].y += odd_term(m, n + 1);
-                d[k].z += odd_term(m, n + 2);
-                d[k].w += odd_term(m, n + 3);
+            for (int j = 0; j < kPart; ++j) {
+              if (p0 + j >= n_parts) break;
+#pragma unroll
+              for (int k = 0; k < kTok; ++k) {
+                d[k].x += p[j][k].x; d[k].y += p[j][k].y; d[k].z += p[j][k].z; d[k].w += p[j][k].w;
               }
-              *reinterpret_cast<uint2*>(args.h + static_cast<int64_t>(m) * args.out + n) =
-                  make_uint2(pack_bf16x2_rn(d[k].x, d[k].y), pack_bf16x2_rn(d[k].z, d[k].w));
             }
           }
-        };
-        if (args.M <= 16) add_up(std::integral_constant<int, 1>{});
-        else add_up(std::integral_constant<int, 4>{});
-      }
-      if (!(ok = dec_sync())) break;                         // parts are read
+#pragma unroll
+          for (int k = 0; k < kTok; ++k) {
+            const int m = m0 + k;
+            if (m >= args.M || n >= args.out) break;
+            if (ticket[c] > 0xFFFF) {                        // some part was marked
+              d[k].x += odd_term(m, n);
+              d[k].y += odd_term(m, n + 1);
+              d[k].z += odd_term(m, n + 2);
+              d[k].w += odd_term(m, n + 3);
+            }
+            *reinterpret_cast<uint2*>(args.h + static_cast<int64_t>(m) * args.out + n) =
+                make_uint2(pack_bf16x2_rn(d[k].x, d[k].y), pack_bf16x2_rn(d[k].z, d[k].w));
+          }
+        }
+      };
+      if (args.M <= 16) add_up(std::integral_constant<int, 1>{});
+      else add_up(std::integral_constant<int, 4>{});
     }
   }
 
