@@ -943,14 +943,16 @@ int check_bwd_args(const uint16_t* dh, const uint16_t* x, const uint16_t* us, in
 // Up to this many tokens the transposed GEMM with a persistent grid runs
 // (gemm_slots_sm100.cuh), above it the CTA-pair GEMM.
 constexpr int64_t kSlotsFewTokens = qnf4::kSgMaxN;
-// The rank-r product takes one CTA per token and four columns while that reads
-// about what it must: few tokens, or adapters that differ from token to token.
-// Otherwise the tensor-core tile, which reads an adapter once per 128 tokens.
-// Measured, one CTA per token / tile: 64 tokens of 64 adapters, 8192 wide,
-// rank 16: 14 / 18 us; 256 tokens of 256 adapters, 4096, rank 16: 17 / 37 us;
-// 256 tokens of 2 adapters, 4096, rank 64: 24 / 14 us.
+// The rank-r product takes one CTA per token and four columns (an adapter read
+// once per four of its tokens) while there are few of them, or when a tile of
+// 128 tokens can hold many adapters: the tensor-core tile reads an adapter once
+// per tile, but multiplies every token with every adapter of its tile.
+// Measured, CTAs per token / tile, us: 16 tokens of one adapter, 8192 wide,
+// rank 16: 12 / 15; 64 tokens of one, 4096, rank 64: 14 / 13; 256 tokens of 2,
+// 4096, rank 64: 30 / 14; 128 tokens of 32, 4096, rank 64: 19 / 17; 256 tokens
+// of 64, 8192, rank 64: 39 / 54; 256 tokens of 256, 4096, rank 16: 18 / 37.
 bool slots_us_per_token(int64_t M, int64_t n_adapters, int r8) {
-  return M <= kSlotsFewTokens && (M * r8 < 4096 || 16 * n_adapters >= M);
+  return M <= kSlotsFewTokens && (M * r8 <= 4096 || n_adapters > 32);
 }
 
 // Workspace of linear_fwd_slots: us [M, r8] bf16; for few tokens the row
@@ -986,7 +988,7 @@ int launch_slots_us(const uint16_t* x, const uint16_t* A, const float* scale, co
   if (slots_us_per_token(M, n_adapters, r8)) {
     LaunchTimer lt_("slots_us", st);
     qnf4::slots_us_kernel<<<static_cast<unsigned>(M * (r8 / qnf4::kUsRanks)), qnf4::kUsThreads, 0, st>>>(
-        x, A, scale, ids, in, n_adapters, r, r8, us, tickets, n_tickets);
+        x, A, scale, ids, static_cast<int>(M), in, n_adapters, r, r8, us, tickets, n_tickets);
     QLORA_CUDA_TRY(cudaGetLastError());
     return QLORA_OK;
   }

@@ -182,65 +182,123 @@ __device__ __noinline__ float slots_odd_term(const uint16_t* B_row, const uint16
   return f;
 }
 
-// us of a few tokens.  One CTA per (token, 4 rank columns): its warps share
-// the K axis (thread t takes the 8-column chunks t, t + 256, ...), then add up
-// over a butterfly and shared memory in warp order.  us has rows of r8 = r
+// us of at most 256 tokens.  One CTA per (token, 4 rank columns): its warps
+// share the K axis (thread t takes the 8-column chunks t, t + 256, ...), then
+// add up over a butterfly and shared memory in warp order.  Tokens of one
+// adapter go in fours, in token order: the CTA of the first of four reads the
+// adapter once for all of them, the other three leave (128 tokens of 64
+// adapters, 28672 wide, rank 16: 31 us each for itself, 24 so; the adapters'
+// and x's bytes out of L2 bound it).  A token's sum is the same in any
+// company.  us has rows of r8 = r
 // rounded up to 8; its columns past r, and the rows of tokens without an
-// adapter, are zero.  Bound by the adapters' bytes, or by latency.  The CTAs
-// also zero the tickets of the GEMM behind, and let it start beside them.
+// adapter, are zero.  The CTAs also zero the tickets of the GEMM behind, and
+// let it start beside them.
 constexpr int kUsThreads = 256;
 constexpr int kUsRanks = 4;
+constexpr int kUsTokens = 4;
 
-__global__ void __launch_bounds__(kUsThreads) slots_us_kernel(
-    const uint16_t* __restrict__ x, const uint16_t* __restrict__ A, const float* __restrict__ scale,
-    const int32_t* __restrict__ ids, int64_t K, int64_t n_adapters, int r, int r8, uint16_t* __restrict__ us,
-    uint32_t* __restrict__ tickets, int n_tickets) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ float sums[kUsThreads / 32][kUsRanks];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = blockIdx.x * kUsThreads + threadIdx.x; i < n_tickets; i += gridDim.x * kUsThreads) tickets[i] = 0u;
-  const int per_tok = r8 / kUsRanks;
-  const int64_t m = blockIdx.x / per_tok;
-  const int j0 = static_cast<int>(blockIdx.x % per_tok) * kUsRanks;
-  const int32_t a = __ldg(ids + m);
-  const bool has = a >= 0 && a < n_adapters;
-  float acc[kUsRanks] = {};
-  if (has) {
-    const uint16_t* Ar = A + (static_cast<int64_t>(a) * r + j0) * K;
-    const int chunks = static_cast<int>(K / 8);
-#pragma unroll 2
-    for (int c = threadIdx.x; c < chunks; c += kUsThreads) {
-      const uint4 xv = ld_nc_v4(x + m * K + c * 8);
-      uint4 av[kUsRanks];
+// acc[i][j] = thread's share of the products of token tok[i] with adapter row j
+template <int kTok>
+__device__ __forceinline__ void slots_us_part(const uint16_t* __restrict__ x, const uint16_t* __restrict__ Ar,
+                                              const int* tok, int64_t K, int rows, float (&acc)[kUsTokens][kUsRanks]) {
+  const int chunks = static_cast<int>(K / 8);
+  const uint16_t* xr[kTok];
 #pragma unroll
-      for (int j = 0; j < kUsRanks; ++j)
-        av[j] = j0 + j < r ? ld_nc_v4(Ar + j * K + c * 8) : make_uint4(0, 0, 0, 0);
-      const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+  for (int i = 0; i < kTok; ++i) xr[i] = x + tok[i] * K;
+#pragma unroll 2
+  for (int c = threadIdx.x; c < chunks; c += kUsThreads) {
+    uint4 xv[kTok], av[kUsRanks];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) xv[i] = ld_nc_v4(xr[i] + c * 8);
+#pragma unroll
+    for (int j = 0; j < kUsRanks; ++j)
+      av[j] = j < rows ? ld_nc_v4(Ar + j * K + c * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const uint32_t xw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
 #pragma unroll
       for (int j = 0; j < kUsRanks; ++j) {
         const uint32_t aw[4] = {av[j].x, av[j].y, av[j].z, av[j].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          acc[j] = fmaf(fewtok_bf16_lo(xw[e]), fewtok_bf16_lo(aw[e]), acc[j]);
-          acc[j] = fmaf(fewtok_bf16_hi(xw[e]), fewtok_bf16_hi(aw[e]), acc[j]);
+          acc[i][j] = fmaf(fewtok_bf16_lo(xw[e]), fewtok_bf16_lo(aw[e]), acc[i][j]);
+          acc[i][j] = fmaf(fewtok_bf16_hi(xw[e]), fewtok_bf16_hi(aw[e]), acc[i][j]);
         }
       }
     }
   }
+}
+
+__global__ void __launch_bounds__(kUsThreads, 3) slots_us_kernel(
+    const uint16_t* __restrict__ x, const uint16_t* __restrict__ A, const float* __restrict__ scale,
+    const int32_t* __restrict__ ids, int M, int64_t K, int64_t n_adapters, int r, int r8, uint16_t* __restrict__ us,
+    uint32_t* __restrict__ tickets, int n_tickets) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float sums[kUsThreads / 32][kUsTokens][kUsRanks];
+  __shared__ uint32_t same[kUsThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = blockIdx.x * kUsThreads + threadIdx.x; i < n_tickets; i += gridDim.x * kUsThreads) tickets[i] = 0u;
+  const int per_tok = r8 / kUsRanks;
+  const int m = static_cast<int>(blockIdx.x) / per_tok;
+  const int j0 = static_cast<int>(blockIdx.x % per_tok) * kUsRanks;
+  const int32_t a = __ldg(ids + m);
+  const int t = static_cast<int>(threadIdx.x);
+  const int32_t other = t < M ? __ldg(ids + t) : -1;         // thread t looks at token t
+  if (a < 0 || a >= n_adapters) {
+    if (t < kUsRanks) us[static_cast<int64_t>(m) * r8 + j0 + t] = 0;
+    return;
+  }
+  const uint32_t hit = __ballot_sync(0xFFFFFFFFu, t < M && other == a);
+  if (lane == 0) same[warp] = hit;
+  __syncthreads();
+  // the tokens of this adapter before this one, and this one with the next three
+  int before = 0, n_tok = 0, tok[kUsTokens];
 #pragma unroll
-  for (int j = 0; j < kUsRanks; ++j) {
+  for (int i = 0; i < kUsTokens; ++i) tok[i] = m;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], off);
-    if (lane == 0) sums[warp][j] = acc[j];
+  for (int w = 0; w < kUsThreads / 32; ++w) {
+    uint32_t bits = same[w];
+    const int base = 32 * w;
+    if (base < m) before += __popc(m - base >= 32 ? bits : bits & ((1u << (m - base)) - 1u));
+    if (base + 31 < m) continue;
+    if (base < m) bits &= ~((1u << (m - base)) - 1u);
+#pragma unroll
+    for (int i = 0; i < kUsTokens; ++i)
+      if (i == n_tok && bits != 0) {
+        tok[i] = base + __ffs(static_cast<int>(bits)) - 1;
+        bits &= bits - 1;
+        ++n_tok;
+      }
+  }
+  if (before % kUsTokens != 0) return;
+  float acc[kUsTokens][kUsRanks] = {};
+  const uint16_t* Ar = A + (static_cast<int64_t>(a) * r + j0) * K;
+  if (n_tok == 1) slots_us_part<1>(x, Ar, tok, K, r - j0, acc);
+  else if (n_tok == 2) slots_us_part<2>(x, Ar, tok, K, r - j0, acc);
+  else slots_us_part<4>(x, Ar, tok, K, r - j0, acc);         // (of three the first stands in for a fourth)
+#pragma unroll
+  for (int i = 0; i < kUsTokens; ++i) {
+    if (i >= n_tok) break;
+#pragma unroll
+    for (int j = 0; j < kUsRanks; ++j) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) acc[i][j] += __shfl_xor_sync(0xFFFFFFFFu, acc[i][j], off);
+      if (lane == 0) sums[warp][i][j] = acc[i][j];
+    }
   }
   __syncthreads();
-  if (threadIdx.x < kUsRanks) {
+  if (t < n_tok * kUsRanks) {
+    const int i = t / kUsRanks, j = t % kUsRanks;
     float v = 0.f;
-    if (has && j0 + static_cast<int>(threadIdx.x) < r) {     // (a NaN in x times a zero of the padding is no result)
-      for (int w = 0; w < kUsThreads / 32; ++w) v += sums[w][threadIdx.x];
+    if (j0 + j < r) {                                        // (a NaN in x times a zero of the padding is no result)
+      for (int w = 0; w < kUsThreads / 32; ++w) v += sums[w][i][j];
       v *= __ldg(scale + a);
     }
-    us[m * r8 + j0 + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    int at = tok[0];
+#pragma unroll
+    for (int k = 1; k < kUsTokens; ++k)
+      if (i == k) at = tok[k];
+    us[static_cast<int64_t>(at) * r8 + j0 + j] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
   }
 }
 
