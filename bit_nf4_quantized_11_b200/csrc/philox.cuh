@@ -9,8 +9,8 @@
 // depends on (seed, offset, row, column) alone, so that the forward and every
 // kernel of the backward draw the same mask and none is stored.
 //
-// Cost: 7 rounds of two 32 x 32 -> 64 multiplications and two 3-input xors per
-// 8 values, about 7 instructions per value with the comparisons.
+// Cost per 8 values: 7 rounds of two 32 x 32 -> 64 multiplications and two
+// 3-input xors, and two or three instructions per value to compare and pack.
 #pragma once
 
 #include "common.cuh"
@@ -31,13 +31,18 @@ __device__ __forceinline__ PhiloxKey philox_key(const uint64_t* state) {
                    static_cast<uint32_t>(off >> 32)};
 }
 
-// The four words for columns 8 group .. 8 group + 7 of a row: the low half of
-// word i decides column 2 i, the high half column 2 i + 1.
-__device__ __forceinline__ void philox_words(const PhiloxKey& key, uint32_t row, uint32_t group, uint32_t (&w)[4]) {
-  uint32_t c0 = group, c1 = row, c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
+// The first product of a column group's rounds.
+constexpr uint64_t kPhiloxA = 0xD2511F53u;
+__device__ __forceinline__ uint64_t philox_first(uint32_t group) { return kPhiloxA * group; }
+
+// The four words for columns 8 group .. 8 group + 7 of a row, from
+// philox_first(group): the low half of word i decides column 2 i, the high
+// half column 2 i + 1.
+__device__ __forceinline__ void philox_words(const PhiloxKey& key, uint32_t row, uint64_t first, uint32_t (&w)[4]) {
+  uint32_t c0 = 0, c1 = row, c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
 #pragma unroll
   for (int i = 0; i < 7; ++i) {
-    const uint64_t a = static_cast<uint64_t>(0xD2511F53u) * c0, b = static_cast<uint64_t>(0xCD9E8D57u) * c2;
+    const uint64_t a = i == 0 ? first : kPhiloxA * c0, b = static_cast<uint64_t>(0xCD9E8D57u) * c2;
     c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
     c1 = static_cast<uint32_t>(b);
     c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
@@ -54,43 +59,55 @@ __device__ __forceinline__ void philox_words(const PhiloxKey& key, uint32_t row,
 __device__ __forceinline__ void philox_drop8(const PhiloxKey& key, uint32_t threshold, uint32_t row, uint32_t group,
                                              uint32_t (&drop)[4]) {
   uint32_t w[4];
-  philox_words(key, row, group, w);
+  philox_words(key, row, philox_first(group), w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) drop[i] = prmt((w[i] & 0xFFFFu) - threshold, (w[i] >> 16) - threshold, 0xFFBBu);
 }
 
-// The drop bits of columns 8 group .. 8 group + 7, shifted into `bits` from
-// below (column 8 group + 7 first): the sign of half - T, one funnel shift each.
+// The keep bits of columns 8 group .. 8 group + 7, shifted into `bits` from
+// below (column 8 group + 7 first): for T > 0, 2^16 half + (2^32 - 2^16 T)
+// carries exactly when half >= T, whatever lies below the half, and an add with
+// carry takes that in: two instructions per value.
 __device__ __forceinline__ uint32_t philox_shift8(const PhiloxKey& key, uint32_t threshold, uint32_t row,
-                                                  uint32_t group, uint32_t bits) {
+                                                  uint64_t first, uint32_t bits) {
   uint32_t w[4];
-  philox_words(key, row, group, w);
+  philox_words(key, row, first, w);
+  const uint32_t lift = 0u - (threshold << 16);
 #pragma unroll
   for (int i = 3; i >= 0; --i) {
-    bits = __funnelshift_l((w[i] >> 16) - threshold, bits, 1);
-    bits = __funnelshift_l((w[i] & 0xFFFFu) - threshold, bits, 1);
+    asm("{\n\t.reg .u32 t;\n\t"
+        "add.cc.u32 t, %1, %2;\n\t"
+        "addc.u32 %0, %0, %0;\n\t"
+        "add.cc.u32 t, %3, %2;\n\t"
+        "addc.u32 %0, %0, %0;\n\t}"
+        : "+r"(bits) : "r"(w[i]), "r"(lift), "r"(w[i] << 16));
   }
-  return bits;
+  return threshold != 0 ? bits : 0xFFFFFFFFu;
 }
 
 // Keep bits of columns 8 group .. 8 group + 7 of a row, bit i for column i.
 __device__ __forceinline__ uint32_t philox_keep8(const PhiloxKey& key, uint32_t threshold, uint32_t row,
                                                  uint32_t group) {
-  return ~philox_shift8(key, threshold, row, group, 0u) & 0xFFu;
+  return philox_shift8(key, threshold, row, philox_first(group), 0u) & 0xFFu;
 }
 
-// Keep bits of the 32 columns from 8-column group `group` on.
+// Keep bits of the 32 columns from 8-column group `group` on.  The first
+// product of the next group is the last one plus a constant.
 __device__ __forceinline__ uint32_t philox_keep32(const PhiloxKey& key, uint32_t threshold, uint32_t row,
                                                   uint32_t group) {
+  const uint64_t first = philox_first(group);
   uint32_t bits = 0;
 #pragma unroll
-  for (int i = 3; i >= 0; --i) bits = philox_shift8(key, threshold, row, group + i, bits);
-  return ~bits;
+  for (int i = 3; i >= 0; --i) bits = philox_shift8(key, threshold, row, first + i * kPhiloxA, bits);
+  return bits;
 }
 
 // The mask as bits, [M, n / 8] (the layout of the calls that take a mask):
-// one 32-bit word per thread and step.  n % 32 == 0.  Bound by the integer
-// pipe (about 260 operations per word), not by its M n / 8 bytes.
+// one 32-bit word per thread and step.  n % 32 == 0.  Bound by the 64-bit
+// products, not by its M n / 8 bytes: of the 14 of a group, those that the four
+// groups of a word share leave 11.5, and 8192 x 11008 values take 33.4 us,
+// which is 15 of them per clock and SM (the add-with-carry packing took the
+// rest out of the way: 35.4 us with two operations more per value).
 __global__ void __launch_bounds__(256) keep_bits_kernel(DropoutRng rng, int64_t M, int64_t n, uint32_t* bits) {
   const PhiloxKey key = philox_key(rng.state);
   const int64_t words = n / 32, total = M * words;
