@@ -106,7 +106,7 @@ __device__ __forceinline__ uint32_t philox_keep32(const PhiloxKey& key, uint32_t
 // one 32-bit word per thread and step.  n % 32 == 0.  Bound by the 64-bit
 // products, not by its M n / 8 bytes: of the 14 of a group, those that the four
 // groups of a word share leave 11.5, and 8192 x 11008 values take 33.4 us,
-// which is 15 of them per clock and SM (the add-with-carry packing took the
+// which is 14 of them per clock and SM (the add-with-carry packing took the
 // rest out of the way: 35.4 us with two operations more per value).
 __global__ void __launch_bounds__(256) keep_bits_kernel(DropoutRng rng, int64_t M, int64_t n, uint32_t* bits) {
   const PhiloxKey key = philox_key(rng.state);
