@@ -189,14 +189,17 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 // Whether a phase is complete, without waiting: asked early, looked at late.
-__device__ __forceinline__ uint32_t mbar_probe(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ uint32_t mbar_probe(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -346,10 +349,14 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
 
   // Bounded wait; false once it, or any other wait of the CTA, ran out of time.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return mbar_probe(bar, parity) != 0 || sg_wait(smem_u32(bar), parity, tmo, abort_flag);
+    return mbar_probe(smem_u32(bar), parity) != 0 || sg_wait(smem_u32(bar), parity, tmo, abort_flag);
   };
   // the same answer for every lane of a warp (the roles that work as whole warps)
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+  // by address, after a probe that was taken earlier
+  auto settled = [&](uint32_t probed, uint32_t bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, probed || mbar_probe(bar, parity) || sg_wait(bar, parity, tmo, abort_flag)) != 0;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ x tiles
@@ -520,7 +527,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       dph ^= 1u;
       return done;
     };
-    int uu = uu0, tile = tile0, seg = 0, cs = 0, seg_uu = uu0;
+    int uu = uu0, tile = tile0, seg = 0, seg_uu = uu0;
     uint32_t cph = 0;
     // The CTA's first and last tile, cut between CTAs or not: which CTAs hold
     // units of them.  Found here, while the first codes are on their way.
@@ -537,18 +544,22 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
     // block before it completes.
     uint32_t c[8];
     float c_hat = 0.f;
-    auto settled = [&](uint32_t probed, uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xFFFFFFFFu, probed) != 0 || wait_warp(bar, parity);
-    };
+    const uint32_t sfull_a = smem_u32(sfull), cempty_a = smem_u32(cempty), afull_a = smem_u32(afull),
+                   aempty_a = smem_u32(aempty);
+    const uint32_t codes_a = smem_u32(c_ring) + t * 128 + (((2 * g) ^ (t & 7)) << 4);      // the block's two 16-byte chunks:
+    const uint32_t scale_a = smem_u32(s_ring) + (g * kSgRows + t) * 4;                     // here and 16 bytes across
+    uint32_t cs_codes = codes_a, cs_scale = scale_a, cs_bar = 0;                           // of the ring's slot in turn
     auto read_codes = [&](uint32_t probed) {
-      if (!settled(probed, sfull + cs, cph)) return false;
-      const uint32_t crow = smem_u32(c_ring + cs * kSgCodeTile) + t * 128;
-      lds_v4(crow + (((2 * g) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[0]));
-      lds_v4(crow + (((2 * g + 1) ^ (t & 7)) << 4), *reinterpret_cast<uint32_t(*)[4]>(&c[4]));
-      c_hat = s_ring[(cs * 4 + g) * kSgRows + t];
+      if (!settled(probed, sfull_a + cs_bar, cph)) return false;
+      lds_v4(cs_codes, *reinterpret_cast<uint32_t(*)[4]>(&c[0]));
+      lds_v4(cs_codes ^ 16u, *reinterpret_cast<uint32_t(*)[4]>(&c[4]));
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(c_hat) : "r"(cs_scale));
       __syncwarp();
-      if (lane == 0) mbar_arrive(cempty + cs);
-      if (++cs == kSgUnits) { cs = 0; cph ^= 1u; }
+      if (lane == 0) mbar_arrive_at(cempty_a + cs_bar);
+      cs_codes += kSgCodeTile;
+      cs_scale += kSgRows * 16;
+      cs_bar += 8;
+      if (cs_bar == 8 * kSgUnits) { cs_codes = codes_a; cs_scale = scale_a; cs_bar = 0; cph ^= 1u; }
       return true;
     };
     bool ok = true;
@@ -559,7 +570,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       const uint32_t a_blk = a_lane + (sa * KB + ib) * 32, a_par = ((it / SA) & 1u) ^ 1u;
       uint32_t next = 0;                                     // its codes are there
       if (kLut && uu < UB) {
-        const uint32_t free = mbar_probe(aempty + sa, a_par);
+        const uint32_t free = mbar_probe(aempty_a + 8 * sa, a_par);
         uint64_t c2;
         asm("mov.b64 %0, {%1, %1};" : "=l"(c2) : "f"(c_hat));
         uint64_t lv[4][8];
@@ -586,9 +597,9 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
         convert(0);
         lookup(2);
         convert(1);
-        if (!(ok = settled(free, aempty + sa, a_par))) break;
+        if (!(ok = settled(free, aempty_a + 8 * sa, a_par))) break;
         tmem_st_32x32b_x16(a_blk, w);
-        if (more) next = mbar_probe(sfull + cs, cph);
+        if (more) next = mbar_probe(sfull_a + cs_bar, cph);
         lookup(3);
         convert(2);
         convert(3);
@@ -667,7 +678,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
       tmem_st_wait();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(afull + sa);
+      if (lane == 0) mbar_arrive_at(afull_a + 8 * sa);
       if (SA > S && uu < UB && !(ok = x_done(it))) break;
 
       if (++uu != UPT && i != n_u - 1) continue;
