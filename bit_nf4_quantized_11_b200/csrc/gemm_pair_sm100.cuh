@@ -465,6 +465,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
       const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + sub * 256;
       for (int a = 0; a < 2; ++a) {
         const int col0 = a * 128 + (part & 1) * 64;         // this warp's 64 columns of half a
+        const uint64_t first = philox_first(static_cast<uint32_t>((n0 + col0) / 8));
         uint32_t base[64];
         tmem_ld_32x32b_x32(lanes + col0, *reinterpret_cast<uint32_t(*)[32]>(&base[0]));
         tmem_ld_32x32b_x32(lanes + col0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&base[32]));
@@ -480,8 +481,7 @@ qlora_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_act,
           tmem_ld_32x32b_x16(lanes + col0 + 16 * c, p);
 #pragma unroll
           for (int g = 0; g < 2; ++g)
-            philox_drop8(key, slots.rng.threshold, static_cast<uint32_t>(m),
-                         static_cast<uint32_t>((n0 + col0) / 8 + 2 * c + g), drop[g]);
+            philox_drop8(key, slots.rng.threshold, static_cast<uint32_t>(m), first + (2 * c + g) * kPhiloxA, drop[g]);
           tmem_ld_wait();
           uint32_t o[8];
 #pragma unroll

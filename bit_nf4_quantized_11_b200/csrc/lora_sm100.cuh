@@ -321,10 +321,10 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
         const int tok = kCol ? k0 + (i & 63) : row0 + i;
         const int f0 = kCol ? row0 + 64 * (i >> 6) : k0;
         uint32_t drop[4][4];
+        const uint64_t first = philox_first(static_cast<uint32_t>(f0 / 8 + 4 * q));
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          philox_drop8(key, args.rng.threshold, static_cast<uint32_t>(tok), static_cast<uint32_t>(f0 / 8 + 4 * q + c),
-                       drop[c]);
+          philox_drop8(key, args.rng.threshold, static_cast<uint32_t>(tok), first + c * kPhiloxA, drop[c]);
         wait(full + s, (it / S) & 1u);
         if (*abort_flag) break;
         const uint32_t rbase = smem_u32(a_ring + s * kLrAStage) + row_off;

@@ -31,7 +31,8 @@ __device__ __forceinline__ PhiloxKey philox_key(const uint64_t* state) {
                    static_cast<uint32_t>(off >> 32)};
 }
 
-// The first product of a column group's rounds.
+// The first product of a column group's rounds; the next group's is this one
+// plus kPhiloxA.
 constexpr uint64_t kPhiloxA = 0xD2511F53u;
 __device__ __forceinline__ uint64_t philox_first(uint32_t group) { return kPhiloxA * group; }
 
@@ -56,10 +57,10 @@ __device__ __forceinline__ void philox_words(const PhiloxKey& key, uint32_t row,
 // Those columns as bf16x2 masks of the dropped values (all ones in a dropped
 // half): half - T is negative exactly when the half is dropped, and a prmt
 // that replicates signs widens the two signs to halves.
-__device__ __forceinline__ void philox_drop8(const PhiloxKey& key, uint32_t threshold, uint32_t row, uint32_t group,
+__device__ __forceinline__ void philox_drop8(const PhiloxKey& key, uint32_t threshold, uint32_t row, uint64_t first,
                                              uint32_t (&drop)[4]) {
   uint32_t w[4];
-  philox_words(key, row, philox_first(group), w);
+  philox_words(key, row, first, w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) drop[i] = prmt((w[i] & 0xFFFFu) - threshold, (w[i] >> 16) - threshold, 0xFFBBu);
 }
@@ -91,8 +92,7 @@ __device__ __forceinline__ uint32_t philox_keep8(const PhiloxKey& key, uint32_t 
   return philox_shift8(key, threshold, row, philox_first(group), 0u) & 0xFFu;
 }
 
-// Keep bits of the 32 columns from 8-column group `group` on.  The first
-// product of the next group is the last one plus a constant.
+// Keep bits of the 32 columns from 8-column group `group` on.
 __device__ __forceinline__ uint32_t philox_keep32(const PhiloxKey& key, uint32_t threshold, uint32_t row,
                                                   uint32_t group) {
   const uint64_t first = philox_first(group);
