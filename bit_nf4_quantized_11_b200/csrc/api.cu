@@ -1178,7 +1178,11 @@ int launch_us_rng(const uint16_t* x, const uint16_t* A, uint16_t* us, int64_t M,
   a.timeout_ns = g_timeout_ns.load();
   const int64_t stages = cdiv(in, 64);
   const LrShape sh = lr_shape(tiles, stages, a.N, false);
-  const int ks = std::min(sh.ks, 4);           // as with a stored mask (launch_lora_row)
+  // A CTA draws its masks at the pace of its SM's products, so K is split
+  // further than with a stored mask (launch_lora_row) while the clusters of 8
+  // surely fit at once (of 16 tiles only 15 do): 4096 wide, 64 / 1024 / 2048
+  // tokens: 15.7 / 16.4 / 28.2 us with clusters of 8, 22.0 / 23.5 / 22.7 with 4.
+  const int ks = 10 * tiles * sh.ks <= 8 * device_sm_count() ? sh.ks : std::min(sh.ks, 4);
   a.ring = sh.ring;
   a.n_alloc = lr_rng_alloc(a.N, false, a.ring, static_cast<int64_t>(tiles) * ks);
   a.stages_per_split = static_cast<int>(cdiv(stages, ks));
