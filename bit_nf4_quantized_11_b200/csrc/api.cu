@@ -956,7 +956,7 @@ bool slots_us_per_token(int64_t M, int64_t n_adapters, int r8) {
 }
 
 // Workspace of linear_fwd_slots: us [M, r8] bf16; for few tokens the row
-// tiles' tickets and the fp32 partials of tiles cut between CTAs, for more the
+// tiles' tickets (and one more for a rank-r kernel before) and the fp32 partials of tiles cut between CTAs, for more the
 // adapter lists of the token tiles.
 struct SlotsWs {
   size_t ticket_off, part_off, tiles_off, total;
@@ -975,7 +975,7 @@ SlotsWs slots_ws(int64_t M, int64_t in, int64_t out, int r) {
     w.total = w.tiles_off + round256(static_cast<size_t>(cdiv(M, qnf4::kSlotsTile)) * sizeof(qnf4::SlotsTile));
     return w;
   }
-  w.part_off = w.ticket_off + round256(static_cast<size_t>(cdiv(out, qnf4::kSgRows)) * 4);
+  w.part_off = w.ticket_off + round256(static_cast<size_t>(cdiv(out, qnf4::kSgRows) + 1) * 4);
   const size_t N = static_cast<size_t>(cdiv(M, 16) * 16);
   w.total = w.part_off + static_cast<size_t>(slots_ctas(in, out)) * 2 * N * qnf4::kSgRows * 4;
   return w;
@@ -1253,9 +1253,9 @@ int launch_grads_rng(const uint16_t* dh, const uint16_t* us, const uint16_t* x, 
 }
 
 // Forward workspace: for few tokens those of the transposed GEMM, then the
-// few-token rank-r partials and ticket; then the padded copies (r % 8 != 0).
+// few-token rank-r partials; then the padded copies (r % 8 != 0).
 size_t fwd_rng_base_ws(int64_t M, int64_t in, int64_t out, int r) {
-  return M <= kSlotsFewTokens ? slots_ws(M, in, out, r).total + fewtok_ws(in, r) : 0;
+  return M <= kSlotsFewTokens ? slots_ws(M, in, out, r).total + fewtok_ws(in, r) - 256 : 0;
 }
 
 size_t fwd_rng_ws(int64_t M, int64_t in, int64_t out, int r) {
@@ -1274,14 +1274,19 @@ int linear_fwd_rng_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* w,
                         const uint16_t* B, int r, float s_lora, const qnf4::DropoutRng& rng, uint16_t* h,
                         uint16_t* us, void* workspace, cudaStream_t st) {
   const int64_t in = w->cols, out = w->rows;
+  const SlotsWs sw = slots_ws(M, in, out, r);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  const bool few = M <= kSlotsFewTokens;
+  uint32_t* tickets = few ? reinterpret_cast<uint32_t*>(base + sw.ticket_off) : nullptr;
+  const int64_t row_tiles = cdiv(out, qnf4::kSgRows);
+  if (few)
+    QLORA_CUDA_TRY(cudaMemsetAsync(tickets, 0, static_cast<size_t>(row_tiles + 1) * 4, st));
   if (M > 16) {
     const int rc = launch_us_rng(x, A, us, M, in, r, s_lora, rng, st);
     if (rc != QLORA_OK) return rc;
   } else {
-    uint8_t* ft = static_cast<uint8_t*>(workspace) + slots_ws(M, in, out, r).total;
-    float* part = reinterpret_cast<float*>(ft);
-    unsigned int* ticket = reinterpret_cast<unsigned int*>(ft + fewtok_ws(in, r) - 256);
-    QLORA_CUDA_TRY(cudaMemsetAsync(ticket, 0, sizeof(unsigned int), st));
+    float* part = reinterpret_cast<float*>(base + sw.total);
+    unsigned int* ticket = tickets + row_tiles;
     const unsigned chunks = static_cast<unsigned>(cdiv(in, qnf4::kFtChunk));
     {
       LaunchTimer lt_("lora_fewtok", st);
@@ -1294,11 +1299,7 @@ int linear_fwd_rng_impl(const uint16_t* x, int64_t M, const qlora_nf4_weight* w,
     }
     QLORA_CUDA_TRY(cudaGetLastError());
   }
-  if (M > kSlotsFewTokens) return launch_gemm(false, w, x, M, in, us, B, r, h, out, st);   // h = [x|us] [W0|B]^T
-  const SlotsWs sw = slots_ws(M, in, out, r);
-  uint8_t* base = static_cast<uint8_t*>(workspace);
-  uint32_t* tickets = reinterpret_cast<uint32_t*>(base + sw.ticket_off);
-  QLORA_CUDA_TRY(cudaMemsetAsync(tickets, 0, static_cast<size_t>(cdiv(out, qnf4::kSgRows)) * 4, st));
+  if (!few) return launch_gemm(false, w, x, M, in, us, B, r, h, out, st);   // h = [x|us] [W0|B]^T
   return launch_slots_gemm(x, M, w, B, 1, r, us, nullptr, h, reinterpret_cast<float*>(base + sw.part_off), tickets,
                            false, st);
 }
