@@ -113,6 +113,13 @@ def test_one_adapter_equals_every_token(cuda_lib, M):
     check(cuda_lib, M, 512, 448, 16, 6, np.full(M, 4), seed=M)
 
 
+@pytest.mark.parametrize("r,n", [(12, 9), (16, 40), (64, 40)])
+def test_groups_of_one_to_nine_tokens(cuda_lib, r, n):
+    """Adapter k has k + 1 tokens, in any order: full and partial groups of tokens that share an adapter's reading."""
+    ids = np.random.default_rng(r).permutation(np.repeat(np.arange(9), np.arange(1, 10)))
+    check(cuda_lib, len(ids), 576, 192, r, n, ids, seed=r + n)
+
+
 @pytest.mark.parametrize("M,n_in,n_out,r,n", [(12, 512, 320, 16, 5), (90, 512, 320, 16, 5), (600, 512, 320, 16, 5)])
 def test_unused_adapters_may_hold_anything(cuda_lib, M, n_in, n_out, r, n):
     """Infinities and NaN in slots that no token uses, and next to the used
