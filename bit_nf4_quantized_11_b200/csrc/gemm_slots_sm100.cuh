@@ -598,6 +598,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
         lookup(2);
         convert(1);
         if (!(ok = settled(free, aempty_a + 8 * sa, a_par))) break;
+        tc_fence_after_sync();                               // the UMMAs that read the slot, before the store over it
         tmem_st_32x32b_x16(a_blk, w);
         if (more) next = mbar_probe(sfull_a + cs_bar, cph);
         lookup(3);
@@ -616,6 +617,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
           }
         }
         if (!(ok = wait_warp(aempty + sa, a_par))) break;
+        tc_fence_after_sync();
         tmem_st_32x32b_x32(a_blk, v);
       } else {
         uint32_t v[32];
@@ -644,6 +646,7 @@ slots_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_con
           if (j0 == args.r8) { j0 = 0; ++li; }
         }
         if (!(ok = wait_warp(aempty + sa, a_par))) break;
+        tc_fence_after_sync();
         if (SA > S && !(ok = x_done(it))) break;
         grid_dependency_wait();                              // us comes from the kernel before
         // the tokens' us under the columns of their own adapter, zero elsewhere

@@ -277,3 +277,18 @@ def test_two_calls_at_once_and_graphs_that_share_a_workspace(cuda_lib):
             torch.cuda.synchronize()
             assert torch.equal(out, h)
     assert q.last_device_status() == 0
+
+
+@pytest.mark.parametrize("M,n_in,n_out", [(8, 8192, 128), (64, 4160, 192), (100, 8192, 192), (200, 4160, 128)])
+def test_long_rows_refill_the_operand_ring(cuda_lib, M, n_in, n_out):
+    """Rows of 65 to 128 blocks go through the eight-block tensor-memory ring
+    many times; the products that read a slot are over before it is written
+    anew, so every run has the same bits."""
+    q = cuda_lib
+    ids = mixed(M, 3, M)
+    h0 = check(q, M, n_in, n_out, 16, 3, ids, seed=M)
+    W, x, A, B, scale = (t.cuda() for t in make(M, n_in, n_out, 16, 3, M))
+    w = q.quantize_nf4(W)
+    ids_t = torch.from_numpy(ids.astype(np.int32)).cuda()
+    for _ in range(20):
+        assert torch.equal(h0, q.linear_fwd_slots(x, w, A, B, scale, ids_t))
