@@ -81,7 +81,7 @@ __device__ __forceinline__ uint32_t philox_shift8(const PhiloxKey& key, uint32_t
         "addc.u32 %0, %0, %0;\n\t"
         "add.cc.u32 t, %3, %2;\n\t"
         "addc.u32 %0, %0, %0;\n\t}"
-        : "+r"(bits) : "r"(w[i]), "r"(lift), "r"(w[i] << 16));
+        : "+&r"(bits) : "r"(w[i]), "r"(lift), "r"(w[i] << 16));    // (bits is written before the last input is read)
   }
   return threshold != 0 ? bits : 0xFFFFFFFFu;
 }

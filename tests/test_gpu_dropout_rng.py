@@ -49,6 +49,27 @@ def test_keep_bits(cuda_lib, seed, offset, p, M, n):
         assert np.array_equal(got[m], np.packbits(k, axis=1, bitorder="little")[:, 0])
 
 
+@pytest.mark.parametrize("p", [1 / 65536, 0.25, 0.5, 32769 / 65536, 65534 / 65536, 65535 / 65536])
+def test_keep_bits_of_a_whole_mask(cuda_lib, p):
+    """262144 values per threshold, each half of a word four times on average:
+    the comparison holds on both sides of T, at its ends too."""
+    M, n, seed, offset = 64, 4096, 0x0123456789ABCDEF, 42
+    u = np.uint64
+    m32, sh = u(0xFFFFFFFF), u(32)
+    c0, c1 = np.meshgrid(np.arange(n // 8, dtype=u), np.arange(M, dtype=u))
+    c2, c3 = np.full_like(c0, u(offset)), np.zeros_like(c0)
+    k0, k1 = u(seed) & m32, u(seed) >> sh
+    for _ in range(7):
+        a, b = c0 * u(philox.M0), c2 * u(philox.M1)
+        c0, c1, c2, c3 = (b >> sh) ^ c1 ^ k0, b & m32, (a >> sh) ^ c3 ^ k1, a & m32
+        k0, k1 = (k0 + u(philox.W0)) & m32, (k1 + u(philox.W1)) & m32
+    words = np.stack([c0, c1, c2, c3], -1)
+    halves = np.stack([words & u(0xFFFF), words >> u(16)], -1).reshape(M, n)
+    keep = halves >= u(round(p * 65536))
+    got = cuda_lib.dropout_keep_bits(rng_tensor(seed, offset), p, M, n).cpu().numpy()
+    assert np.array_equal(got, np.packbits(keep, axis=1, bitorder="little"))
+
+
 def run(q, M, n_in, n_out, r, alpha, p, seed=0, sample=None):
     prob = synth.problem(M, n_in, n_out, r, seed=seed)
     dev = torch.device("cuda")
