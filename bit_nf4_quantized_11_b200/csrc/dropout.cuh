@@ -154,8 +154,10 @@ __global__ void __launch_bounds__(kDxThreads) dropout_dx_kernel(
     for (int e2 = 0; e2 < 4; ++e2) {
       const float k0 = (kb >> (2 * e2)) & 1u ? inv_keep : 0.f;
       const float k1 = (kb >> (2 * e2 + 1)) & 1u ? inv_keep : 0.f;
-      const float v0 = __fadd_rn(__uint_as_float(dw[e2] << 16), __fmul_rn(k0, pv[2 * e2]));
-      const float v1 = __fadd_rn(__uint_as_float(dw[e2] & 0xFFFF0000u), __fmul_rn(k1, pv[2 * e2 + 1]));
+      // (kRng: a dropped column adds nothing, whatever its P is)
+      const float p0 = kRng && k0 == 0.f ? 0.f : pv[2 * e2], p1 = kRng && k1 == 0.f ? 0.f : pv[2 * e2 + 1];
+      const float v0 = __fadd_rn(__uint_as_float(dw[e2] << 16), __fmul_rn(k0, p0));
+      const float v1 = __fadd_rn(__uint_as_float(dw[e2] & 0xFFFF0000u), __fmul_rn(k1, p1));
       o[e2] = pack_bf16x2_rn(v0, v1);
     }
     *reinterpret_cast<uint4*>(dx + m * n + i) = make_uint4(o[0], o[1], o[2], o[3]);

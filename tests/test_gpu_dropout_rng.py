@@ -324,3 +324,32 @@ def test_infinities_in_dropped_places_change_nothing(cuda_lib):
         _, us1 = q.linear_fwd_dropout_rng(bad, w, A, B, 32.0, rng, 0.3)
         _, dA1, dB1 = q.linear_bwd_dropout_rng(dh, bad, us1, w, A, B, 32.0, rng, 0.3)
         assert torch.equal(us, us1) and torch.equal(dA, dA1) and torch.equal(dB, dB1)
+
+
+@pytest.mark.parametrize("M", [12, 300])
+@pytest.mark.parametrize("r", [16, 136])
+def test_a_dropped_column_of_dx_is_the_base_product(cuda_lib, M, r):
+    """Where the mask drops an input, dx is dh W0 whatever the adapter's
+    product is there, an infinity or NaN too; a kept one does see it."""
+    q = cuda_lib
+    prob = synth.problem(M, 256, 192, r, seed=M + r)
+    w = q.quantize_nf4(prob["W"].cuda())
+    x, A, B, dh = (prob[k].cuda() for k in ("x", "A", "B", "dh"))
+    rng, p = rng_tensor(9, M), 0.3
+    bits = q.dropout_keep_bits(rng, p, M, 256).cpu().numpy()
+    keep = torch.from_numpy(linear.unpack_keep(bits, 256) == 1).cuda()
+    us = torch.zeros(M, r, dtype=torch.bfloat16, device="cuda")
+    base, _, _ = q.linear_bwd_dropout_rng(dh, x, us, w, torch.zeros_like(A), B, 32.0, rng, p)
+    fine, _, _ = q.linear_bwd_dropout_rng(dh, x, us, w, A, B, 32.0, rng, p)
+    assert torch.equal(fine[~keep], base[~keep])
+    bad = A.clone()
+    bad[3, 40:60] = float("inf")
+    dx, _, _ = q.linear_bwd_dropout_rng(dh, x, us, w, bad, B, 32.0, rng, p)
+    assert torch.equal(dx[~keep], base[~keep])
+    hit = torch.zeros_like(keep)
+    hit[:, 40:60] = True
+    assert not bool(dx[keep & hit].isfinite().any()) and torch.equal(dx[keep & ~hit], fine[keep & ~hit])
+    bad = B.clone()
+    bad[5, 2] = float("nan")
+    dx, _, _ = q.linear_bwd_dropout_rng(dh, x, us, w, A, bad, 32.0, rng, p)
+    assert torch.equal(dx[~keep], base[~keep]) and bool(dx[keep].isnan().all())
