@@ -1238,18 +1238,27 @@ int launch_grads_rng(const uint16_t* dh, const uint16_t* us, const uint16_t* x, 
   a.ring = sh.ring;
   const int64_t tiles = t_dB + t_dA;
   a.n_alloc = lr_rng_alloc(a.N, true, a.ring, tiles * ks);
-  // at most 8 stages (32 steps of the tensor cores' sum) per accumulator, as
-  // far as the cluster goes
+  // at most 8 stages (32 steps of the tensor cores' sum) per accumulator: the
+  // cluster grows as far as it goes, then several launches share the tokens
   while (ks < 8 && cdiv(stages, ks) > 8 * lr_rng_accumulators(a.N, a.n_alloc)) {
     ks *= 2;
     a.n_alloc = lr_rng_alloc(a.N, true, a.ring, tiles * ks);
   }
-  a.stages_per_split = static_cast<int>(cdiv(stages, ks));
+  // (8192 tokens or more a launch once ks is 8; the gradients are read and
+  // written once more for each, 8 r (in + out) bytes)
+  const int64_t most = ks * 8ll * lr_rng_accumulators(a.N, a.n_alloc);
   CUtensorMap tm[4];
   if (!make_tmap_bf16(&tm[0], dh, M, out, 64) || !make_tmap_bf16(&tm[1], us, M, r, 64) ||
       !make_tmap_bf16(&tm[2], x, M, in, 64) || !make_tmap_bf16(&tm[3], du, M, cols, 64))
     return QLORA_ERR_CUDA;
-  return launch_lora_umma<true, true, true>(tm, a, ks, static_cast<unsigned>(t_dB + t_dA), "lora_colwise", st);
+  int rc = QLORA_OK;
+  for (int64_t s0 = 0; s0 < stages && rc == QLORA_OK; s0 += most) {
+    a.stage0 = static_cast<int>(s0);
+    a.n_stages = static_cast<int>(std::min(most, stages - s0));
+    a.stages_per_split = static_cast<int>(cdiv(a.n_stages, ks));
+    rc = launch_lora_umma<true, true, true>(tm, a, ks, static_cast<unsigned>(t_dB + t_dA), "lora_colwise", st);
+  }
+  return rc;
 }
 
 // Forward workspace: for few tokens those of the transposed GEMM, then the

@@ -43,8 +43,11 @@
 //     most 80 ranks per column group so that 3 x 80 <= 256), dA multiplies by
 //     all three and adds the three results.
 //   * The tensor cores cut the fp32 sum at every step, always towards zero:
-//     after 256 steps of 16 tokens the error was 4e-6.  The stages take turns
-//     over several accumulators, which the epilogue adds up.
+//     of positive products, 391 steps of 16 tokens lost 1e-5 and 1024 steps
+//     4e-5.  The stages take turns over several accumulators,
+//     which the epilogue adds up, and in the col form a launch gives each of
+//     them at most 32 steps (the host's launch_grads_rng): what is left of the
+//     tokens goes to further launches, which add to the gradients.
 #pragma once
 
 #include "common.cuh"
@@ -84,6 +87,8 @@ struct LrProblem {
 struct LrArgs {
   LrProblem p[2];        // blockIdx.x < p[0].tiles: problem 0, else problem 1
   int K;                 // contraction length (row form: features; col form: tokens)
+  int stage0;            // (kRng, col form) the launch's first 64-wide contraction stage
+  int n_stages;          // and how many it takes; further launches add theirs
   int r;                 // rank
   int N;                 // r rounded up to 16
   int n_alloc;           // TMEM columns (power of two >= 32, >= N)
@@ -163,8 +168,9 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
   const int row0 = tile * kLrTileRows;
   const int ks = static_cast<int>(gridDim.y);
   const int split = static_cast<int>(blockIdx.y);
-  const int n_stages_total = (args.K + 63) / 64;
-  const int st_begin = split * args.stages_per_split;
+  const int stage0 = kRng && kCol ? args.stage0 : 0;
+  const int n_stages_total = kRng && kCol ? stage0 + args.n_stages : (args.K + 63) / 64;
+  const int st_begin = stage0 + split * args.stages_per_split;
   const int st_end = min(n_stages_total, st_begin + args.stages_per_split);
   const int n_iter = max(0, st_end - st_begin);
   const uint64_t tmo = args.timeout_ns;
@@ -482,16 +488,25 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     } else if (!kCol) {
       uint16_t* o = static_cast<uint16_t*>(p_out) + static_cast<int64_t>(grow) * args.r + c4 * 4;
       *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2_rn(t.x * sc, t.y * sc), pack_bf16x2_rn(t.z * sc, t.w * sc));
-    } else if (!p_transpose) {
-      float* o = static_cast<float*>(p_out) + static_cast<int64_t>(grow) * args.r + c4 * 4;
-      *reinterpret_cast<float4*>(o) = make_float4(t.x * sc, t.y * sc, t.z * sc, t.w * sc);
     } else {
-      const int64_t ld = p_rows;
-      float* o = static_cast<float*>(p_out) + static_cast<int64_t>(kRng ? p_group * p_ranks : 0) * ld;
-      o[static_cast<int64_t>(c4 * 4 + 0) * ld + grow] = t.x * sc;
-      o[static_cast<int64_t>(c4 * 4 + 1) * ld + grow] = t.y * sc;
-      o[static_cast<int64_t>(c4 * 4 + 2) * ld + grow] = t.z * sc;
-      o[static_cast<int64_t>(c4 * 4 + 3) * ld + grow] = t.w * sc;
+      float f[4] = {t.x * sc, t.y * sc, t.z * sc, t.w * sc};
+      if (!p_transpose) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(p_out) + static_cast<int64_t>(grow) * args.r + c4 * 4);
+        if (kRng && stage0 > 0) {                                    // on top of the launches before
+          const float4 was = *o;
+          f[0] += was.x; f[1] += was.y; f[2] += was.z; f[3] += was.w;
+        }
+        *o = make_float4(f[0], f[1], f[2], f[3]);
+      } else {
+        const int64_t ld = p_rows;
+        float* o = static_cast<float*>(p_out) + static_cast<int64_t>((kRng ? p_group * p_ranks : 0) + c4 * 4) * ld + grow;
+        if (kRng && stage0 > 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] += o[i * ld];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i * ld] = f[i];
+      }
     }
   }
   if (ks > 1) cluster_sync_all();                                    // no CTA leaves while others read it

@@ -353,3 +353,35 @@ def test_a_dropped_column_of_dx_is_the_base_product(cuda_lib, M, r):
     bad[5, 2] = float("nan")
     dx, _, _ = q.linear_bwd_dropout_rng(dh, x, us, w, A, bad, 32.0, rng, p)
     assert torch.equal(dx[~keep], base[~keep]) and bool(dx[keep].isnan().all())
+
+
+@pytest.mark.parametrize("M,r", [(8193, 64), (20000, 136), (40000, 16), (100001, 64), (262144, 64)])
+def test_gradients_of_long_batches(cuda_lib, M, r):
+    """The error of dA and dB does not grow with the tokens.  Positive data,
+    where cut bits add up: dh and B are whole numbers up to 15, so that du is
+    exact, and q = 1/2, s = 1 are powers of two.  What is left, in units of
+    2^-23 of the sum: an accumulator takes at most 32 steps, each cutting less
+    than one; the rounded additions, half each, are those of at most 8
+    accumulators, 8 x 3 partial tiles and one launch per 8192 tokens or more."""
+    q = cuda_lib
+    g = torch.Generator(device="cuda").manual_seed(M + r)
+    n = 64
+    w = q.quantize_nf4(synth.problem(1, n, n, 8)["W"].cuda())
+    dh = torch.randint(1, 16, (M, n), generator=g, device="cuda").bfloat16()
+    B = torch.randint(1, 16, (n, r), generator=g, device="cuda").bfloat16()
+    x = (torch.rand(M, n, generator=g, device="cuda") + 1).bfloat16()
+    us = (torch.rand(M, r, generator=g, device="cuda") + 1).bfloat16()
+    A = torch.zeros(r, n, dtype=torch.bfloat16, device="cuda")
+    rng = rng_tensor(3, M)
+    _, dA, dB = q.linear_bwd_dropout_rng(dh, x, us, w, A, B, float(r), rng, 0.5)
+    bits = q.dropout_keep_bits(rng, 0.5, M, n)
+    keep = (bits[:, :, None] >> torch.arange(8, device="cuda")) & 1
+    xd = x.double() * keep.reshape(M, n) * 2
+    tol = 2.0 ** -23 * (32 + (8 + 24 + -(-M // 8192)) / 2)
+    dB_ref = dh.double().T @ us.double()
+    dA_ref = (dh.double() @ B.double()).T @ xd
+    for name, got, ref in (("dB", dB, dB_ref), ("dA", dA, dA_ref)):
+        err = ((got.double() - ref).abs() / ref).max().item()
+        print(name, M, r, err, tol)
+        assert err <= tol, (name, err, tol)
+    assert q.last_device_status() == 0
