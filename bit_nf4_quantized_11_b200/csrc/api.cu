@@ -1164,6 +1164,21 @@ int lr_rng_alloc(int N, bool b_mn_major, int ring, int64_t ctas) {
 
 int lr_rng_accumulators(int N, int n_alloc) { return std::max(1, std::min(8, n_alloc / ((N + 31) / 32 * 32))); }
 
+// Ring, tensor memory and cluster of the launches whose sums are kept to fp32
+// (du, dA, dB; N-major B): at most 8 stages (32 steps of the tensor cores' sum)
+// per accumulator, as far as a cluster of 8 goes.  Returns the cluster's CTAs.
+int lr_rng_split(qnf4::LrArgs& a, int64_t tiles, int64_t stages) {
+  const LrShape sh = lr_shape(tiles, stages, a.N, true);
+  int ks = sh.ks;
+  a.ring = sh.ring;
+  a.n_alloc = lr_rng_alloc(a.N, true, a.ring, tiles * ks);
+  while (ks < 8 && cdiv(stages, ks) > 8 * lr_rng_accumulators(a.N, a.n_alloc)) {
+    ks *= 2;
+    a.n_alloc = lr_rng_alloc(a.N, true, a.ring, tiles * ks);
+  }
+  return ks;
+}
+
 // us = bf16(s (x k) A^T) with the mask drawn.
 int launch_us_rng(const uint16_t* x, const uint16_t* A, uint16_t* us, int64_t M, int64_t in, int r, float s,
                   const qnf4::DropoutRng& rng, cudaStream_t st) {
@@ -1205,15 +1220,13 @@ int launch_du_parts(const uint16_t* dh, const uint16_t* B, uint16_t* du, int64_t
   a.p[1] = a.p[0];
   a.timeout_ns = g_timeout_ns.load();
   const int64_t stages = cdiv(out, 64);
-  const LrShape sh = lr_shape(tiles, stages, a.N, true);
-  a.ring = sh.ring;
-  a.n_alloc = lr_rng_alloc(a.N, true, a.ring, static_cast<int64_t>(tiles) * sh.ks);
-  a.stages_per_split = static_cast<int>(cdiv(stages, sh.ks));
+  const int ks = lr_rng_split(a, tiles, stages);
+  a.stages_per_split = static_cast<int>(cdiv(stages, ks));
   CUtensorMap tm[4];
   if (!make_tmap_bf16(&tm[0], dh, M, out, 128) || !make_tmap_bf16(&tm[1], B, out, r, 64)) return QLORA_ERR_CUDA;
   tm[2] = tm[0];
   tm[3] = tm[1];
-  return launch_lora_umma<false, true, true>(tm, a, sh.ks, static_cast<unsigned>(tiles), "lora_rowwise_du", st);
+  return launch_lora_umma<false, true, true>(tm, a, ks, static_cast<unsigned>(tiles), "lora_rowwise_du", st);
 }
 
 // dB = dh^T us -> [out, r] and dA = du^T (x k) * dA_scale -> [r, in] in one launch, du in parts.
@@ -1233,19 +1246,10 @@ int launch_grads_rng(const uint16_t* dh, const uint16_t* us, const uint16_t* x, 
                            n_dA, 3, groups, gr};
   a.timeout_ns = g_timeout_ns.load();
   const int64_t stages = cdiv(M, 64);
-  const LrShape sh = lr_shape(t_dB + t_dA, stages, a.N, true);
-  int ks = sh.ks;
-  a.ring = sh.ring;
-  const int64_t tiles = t_dB + t_dA;
-  a.n_alloc = lr_rng_alloc(a.N, true, a.ring, tiles * ks);
-  // at most 8 stages (32 steps of the tensor cores' sum) per accumulator: the
-  // cluster grows as far as it goes, then several launches share the tokens
-  while (ks < 8 && cdiv(stages, ks) > 8 * lr_rng_accumulators(a.N, a.n_alloc)) {
-    ks *= 2;
-    a.n_alloc = lr_rng_alloc(a.N, true, a.ring, tiles * ks);
-  }
-  // (8192 tokens or more a launch once ks is 8; the gradients are read and
-  // written once more for each, 8 r (in + out) bytes)
+  const int ks = lr_rng_split(a, t_dB + t_dA, stages);
+  // tokens past 8 stages per accumulator go to further launches (8192 tokens
+  // or more in each; the gradients are read and written once more for it, 8 r
+  // (in + out) bytes)
   const int64_t most = ks * 8ll * lr_rng_accumulators(a.N, a.n_alloc);
   CUtensorMap tm[4];
   if (!make_tmap_bf16(&tm[0], dh, M, out, 64) || !make_tmap_bf16(&tm[1], us, M, r, 64) ||

@@ -385,3 +385,30 @@ def test_gradients_of_long_batches(cuda_lib, M, r):
         print(name, M, r, err, tol)
         assert err <= tol, (name, err, tol)
     assert q.last_device_status() == 0
+
+
+def test_du_of_many_features_and_tokens(cuda_lib):
+    """The error of du does not grow with the tokens either: 28672 features of
+    positive data, so many tokens that their tiles alone fill the chip.  Each
+    column of x holds a single one, so dA shows du itself, column by column.
+    In units of 2^-23: an accumulator takes at most 14 stages of 4 steps, each
+    cutting less than one; the roundings of the sum over at most 8 accumulators
+    and 8 CTAs, of the scale and of the three parts, half each."""
+    q = cuda_lib
+    g = torch.Generator(device="cuda").manual_seed(1)
+    M, n_in, n_out, r = 19200, 64, 28672, 64
+    w = q.quantize_nf4(synth.problem(1, n_in, n_out, 8)["W"].cuda())
+    dh = torch.rand(M, n_out, generator=g, device="cuda").add_(1).bfloat16()
+    B = torch.rand(n_out, r, generator=g, device="cuda").add_(1).bfloat16()
+    rows = torch.arange(n_in, device="cuda") * (M // n_in) + 7
+    x = torch.zeros(M, n_in, dtype=torch.bfloat16, device="cuda")
+    x[rows, torch.arange(n_in, device="cuda")] = 1
+    us = torch.zeros(M, r, dtype=torch.bfloat16, device="cuda")
+    A = torch.zeros(r, n_in, dtype=torch.bfloat16, device="cuda")
+    _, dA, _ = q.linear_bwd_dropout_rng(dh, x, us, w, A, B, float(r), rng_tensor(1, 1), 0.0)
+    ref = (dh[rows].double() @ B.double()).T
+    err = ((dA.double() - ref).abs() / ref).max().item()
+    tol = 2.0 ** -23 * (14 * 4 + (8 + 8 + 4) / 2)
+    print("du", err, tol)
+    assert err <= tol
+    assert q.last_device_status() == 0
