@@ -1165,14 +1165,16 @@ int lr_rng_alloc(int N, bool b_mn_major, int ring, int64_t ctas) {
 int lr_rng_accumulators(int N, int n_alloc) { return std::max(1, std::min(8, n_alloc / ((N + 31) / 32 * 32))); }
 
 // Ring, tensor memory and cluster of the launches whose sums are kept to fp32
-// (du, dA, dB; N-major B): at most 8 stages (32 steps of the tensor cores' sum)
-// per accumulator, as far as a cluster of 8 goes.  Returns the cluster's CTAs.
-int lr_rng_split(qnf4::LrArgs& a, int64_t tiles, int64_t stages) {
+// (du, dA, dB; N-major B): at most `most` stages (4 steps of the tensor cores'
+// sum each) per accumulator, as far as a cluster of 8 goes.
+// There are two accumulators at least: N <= 64 where two CTAs share an SM's
+// tensor memory, N <= 256 of all of it otherwise.  Returns the cluster's CTAs.
+int lr_rng_split(qnf4::LrArgs& a, int64_t tiles, int64_t stages, int most) {
   const LrShape sh = lr_shape(tiles, stages, a.N, true);
   int ks = sh.ks;
   a.ring = sh.ring;
   a.n_alloc = lr_rng_alloc(a.N, true, a.ring, tiles * ks);
-  while (ks < 8 && cdiv(stages, ks) > 8 * lr_rng_accumulators(a.N, a.n_alloc)) {
+  while (ks < 8 && cdiv(stages, ks) > most * lr_rng_accumulators(a.N, a.n_alloc)) {
     ks *= 2;
     a.n_alloc = lr_rng_alloc(a.N, true, a.ring, tiles * ks);
   }
@@ -1220,7 +1222,7 @@ int launch_du_parts(const uint16_t* dh, const uint16_t* B, uint16_t* du, int64_t
   a.p[1] = a.p[0];
   a.timeout_ns = g_timeout_ns.load();
   const int64_t stages = cdiv(out, 64);
-  const int ks = lr_rng_split(a, tiles, stages);
+  const int ks = lr_rng_split(a, tiles, stages, qnf4::kLrRound);
   a.stages_per_split = static_cast<int>(cdiv(stages, ks));
   CUtensorMap tm[4];
   if (!make_tmap_bf16(&tm[0], dh, M, out, 128) || !make_tmap_bf16(&tm[1], B, out, r, 64)) return QLORA_ERR_CUDA;
@@ -1246,23 +1248,13 @@ int launch_grads_rng(const uint16_t* dh, const uint16_t* us, const uint16_t* x, 
                            n_dA, 3, groups, gr};
   a.timeout_ns = g_timeout_ns.load();
   const int64_t stages = cdiv(M, 64);
-  const int ks = lr_rng_split(a, t_dB + t_dA, stages);
-  // tokens past 8 stages per accumulator go to further launches (8192 tokens
-  // or more in each; the gradients are read and written once more for it, 8 r
-  // (in + out) bytes)
-  const int64_t most = ks * 8ll * lr_rng_accumulators(a.N, a.n_alloc);
+  const int ks = lr_rng_split(a, t_dB + t_dA, stages, qnf4::kLrRound / 2);    // (then rounds of kLrRound)
+  a.stages_per_split = static_cast<int>(cdiv(stages, ks));
   CUtensorMap tm[4];
   if (!make_tmap_bf16(&tm[0], dh, M, out, 64) || !make_tmap_bf16(&tm[1], us, M, r, 64) ||
       !make_tmap_bf16(&tm[2], x, M, in, 64) || !make_tmap_bf16(&tm[3], du, M, cols, 64))
     return QLORA_ERR_CUDA;
-  int rc = QLORA_OK;
-  for (int64_t s0 = 0; s0 < stages && rc == QLORA_OK; s0 += most) {
-    a.stage0 = static_cast<int>(s0);
-    a.n_stages = static_cast<int>(std::min(most, stages - s0));
-    a.stages_per_split = static_cast<int>(cdiv(a.n_stages, ks));
-    rc = launch_lora_umma<true, true, true>(tm, a, ks, static_cast<unsigned>(t_dB + t_dA), "lora_colwise", st);
-  }
-  return rc;
+  return launch_lora_umma<true, true, true>(tm, a, ks, static_cast<unsigned>(t_dB + t_dA), "lora_colwise", st);
 }
 
 // Forward workspace: for few tokens those of the transposed GEMM, then the

@@ -44,10 +44,13 @@
 //     all three and adds the three results.
 //   * The tensor cores cut the fp32 sum at every step, always towards zero:
 //     of positive products, 391 steps of 16 tokens lost 1e-5 and 1024 steps
-//     4e-5.  The stages take turns over several accumulators,
-//     which the epilogue adds up, and in the col form a launch gives each of
-//     them at most 32 steps (the host's launch_grads_rng): what is left of the
-//     tokens goes to further launches, which add to the gradients.
+//     4e-5.  The stages take turns over several accumulators, which the
+//     epilogue adds up; in the col form, whose tokens have no end, in rounds of
+//     64 steps each: between two rounds the masking warps add the accumulators
+//     to a total that takes the place of the last one, by rounded additions
+//     (positive products of 262144 tokens, rank 64: 6e-7.  A backward of 65536
+//     tokens, 1024 -> 11008, takes 2.3 ms, 2.1 without rounds and 2.6 with one
+//     launch per round).
 #pragma once
 
 #include "common.cuh"
@@ -58,6 +61,7 @@ namespace qnf4 {
 constexpr int kLrThreads = 128;
 constexpr int kLrMaskThreads = 320;                        // with a keep mask: eight masking warps
 constexpr int kLrMaxStages = 8;
+constexpr int kLrRound = 16;                              // (kRng, col form) stages per accumulator and round
 constexpr int kLrTileRows = 128;
 constexpr int kLrAStage = kLrTileRows * 64 * 2;           // 16 KB: 128 rows x 64 k (or two 64-wide MN atoms)
 
@@ -87,8 +91,6 @@ struct LrProblem {
 struct LrArgs {
   LrProblem p[2];        // blockIdx.x < p[0].tiles: problem 0, else problem 1
   int K;                 // contraction length (row form: features; col form: tokens)
-  int stage0;            // (kRng, col form) the launch's first 64-wide contraction stage
-  int n_stages;          // and how many it takes; further launches add theirs
   int r;                 // rank
   int N;                 // r rounded up to 16
   int n_alloc;           // TMEM columns (power of two >= 32, >= N)
@@ -138,7 +140,9 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
   uint64_t* empty = bars + kLrMaxStages;
   uint64_t* masked = bars + 2 * kLrMaxStages;                        // (keep mask) the stage is masked
   uint64_t* acc_full = bars + 3 * kLrMaxStages;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
+  uint64_t* round_full = acc_full + 1;                               // a round's sums are complete
+  uint64_t* round_empty = acc_full + 2;                              // and added to the total
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -168,12 +172,15 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
   const int row0 = tile * kLrTileRows;
   const int ks = static_cast<int>(gridDim.y);
   const int split = static_cast<int>(blockIdx.y);
-  const int stage0 = kRng && kCol ? args.stage0 : 0;
-  const int n_stages_total = kRng && kCol ? stage0 + args.n_stages : (args.K + 63) / 64;
-  const int st_begin = stage0 + split * args.stages_per_split;
+  const int n_stages_total = (args.K + 63) / 64;
+  const int st_begin = split * args.stages_per_split;
   const int st_end = min(n_stages_total, st_begin + args.stages_per_split);
   const int n_iter = max(0, st_end - st_begin);
   const uint64_t tmo = args.timeout_ns;
+  const bool in_rounds = kRng && kCol && n_acc > 1 && n_iter > kLrRound * n_acc;
+  const int n_live = in_rounds ? n_acc - 1 : n_acc;
+  const int round = in_rounds ? kLrRound * n_live : max(1, n_iter);  // stages of a round
+  const int n_rounds = (max(1, n_iter) + round - 1) / round;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -182,6 +189,8 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
       mbar_init(masked + s, (blockDim.x - 64) / 32);                 // one arrive per masking warp
     }
     mbar_init(acc_full, 1);
+    mbar_init(round_full, 1);
+    mbar_init(round_empty, 8);                                       // the masking warps
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -200,6 +209,33 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
       *abort_flag = 1;
       raise_device_error(1);
     }
+  };
+
+  // Round k's accumulators, and the total so far, added up over the last one:
+  // warps 2-9, two per 32 rows with every other 16 columns each.
+  auto end_round = [&](int k) -> bool {
+    wait(round_full, k & 1u);
+    if (__any_sync(0xFFFFFFFFu, *abort_flag)) return false;
+    tc_fence_after_sync();
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    for (int c0 = 16 * ((warp - 2) >> 2); c0 < p_N; c0 += 32) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(lanes + c0, v);
+      tmem_ld_wait();
+      for (int g = 1; g < n_live + (k > 0 ? 1 : 0); ++g) {
+        uint32_t w[16];
+        tmem_ld_32x32b_x16(lanes + g * acc_stride + c0, w);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+      }
+      tmem_st_32x32b_x16(lanes + n_live * acc_stride + c0, v);
+    }
+    tmem_st_wait();
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(round_empty);
+    return true;
   };
 
   const uint32_t stage_tx = static_cast<uint32_t>(kLrAStage + (kRng ? lr_b_stage(p_N, kBMN) : b_stage));
@@ -239,8 +275,15 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     if (lane == 0) {
       // ------------------------------------------------------------ MMA issuer
       const uint32_t idesc = umma_idesc_bf16_ab(kLrTileRows, p_N, kCol, kBMN);
-      for (int it = 0; it < n_iter; ++it) {
+      int turn = 0, rounds_done = 0;                                 // (kRng) the stage within its round
+      for (int it = 0; it < n_iter; ++it, ++turn) {
         const int s = it % S;
+        if (kRng && kCol && turn == round) {
+          umma_commit(round_full);
+          wait(round_empty, rounds_done & 1u);
+          ++rounds_done;
+          turn = 0;
+        }
         wait(full + s, (it / S) & 1u);
         if (do_mask) wait(masked + s, (it / S) & 1u);
         if (*abort_flag) break;
@@ -254,7 +297,8 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
           const uint64_t bdesc = kBMN ? umma_desc_sw128(b_base + kk * 2048, 8192, 1024)
                                       : umma_desc_sw128(b_base + kk * 32, 16, 1024);
           if (kRng)
-            umma_bf16_ss(tmem_base + (it % n_acc) * acc_stride, adesc, bdesc, idesc, (it >= n_acc || kk > 0) ? 1u : 0u);
+            umma_bf16_ss(tmem_base + (turn % n_live) * acc_stride, adesc, bdesc, idesc,
+                         (turn >= n_live || kk > 0) ? 1u : 0u);
           else
             umma_bf16_ss(tmem_base, adesc, bdesc, idesc, (it > 0 || kk > 0) ? 1u : 0u);
         }
@@ -323,6 +367,7 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
       const uint32_t row_off = (kCol ? (i >> 6) * 8192 : 0) + r * 128;
       for (int it = 0; it < n_iter; ++it) {
         const int s = it % S;
+        if (kCol && it > 0 && it % round == 0 && !end_round(it / round - 1)) break;
         const int k0 = (st_begin + it) * 64;
         const int tok = kCol ? k0 + (i & 63) : row0 + i;
         const int f0 = kCol ? row0 + 64 * (i >> 6) : k0;
@@ -384,6 +429,8 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(masked + s);
     }
+  } else if (kRng && kCol) {
+    for (int k = 0; k + 1 < n_rounds && end_round(k); ++k) {}
   }
 
   // ---------------------------------------------------------------- epilogue
@@ -401,7 +448,10 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + c0, v);
     tmem_ld_wait();
     if (kRng) {
-      for (int g = 1; g < n_acc && g < n_iter; ++g) {
+      // the last round's accumulators, then the total of the rounds before
+      const int n_sets = min(n_live, n_iter - (n_rounds - 1) * round);
+      for (int e = 1; e < n_sets + (n_rounds > 1 ? 1 : 0); ++e) {
+        const int g = e < n_sets ? e : n_live;
         uint32_t w[32];
         tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + g * acc_stride + c0, w);
         tmem_ld_wait();
@@ -488,25 +538,16 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     } else if (!kCol) {
       uint16_t* o = static_cast<uint16_t*>(p_out) + static_cast<int64_t>(grow) * args.r + c4 * 4;
       *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2_rn(t.x * sc, t.y * sc), pack_bf16x2_rn(t.z * sc, t.w * sc));
+    } else if (!p_transpose) {
+      float* o = static_cast<float*>(p_out) + static_cast<int64_t>(grow) * args.r + c4 * 4;
+      *reinterpret_cast<float4*>(o) = make_float4(t.x * sc, t.y * sc, t.z * sc, t.w * sc);
     } else {
-      float f[4] = {t.x * sc, t.y * sc, t.z * sc, t.w * sc};
-      if (!p_transpose) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(p_out) + static_cast<int64_t>(grow) * args.r + c4 * 4);
-        if (kRng && stage0 > 0) {                                    // on top of the launches before
-          const float4 was = *o;
-          f[0] += was.x; f[1] += was.y; f[2] += was.z; f[3] += was.w;
-        }
-        *o = make_float4(f[0], f[1], f[2], f[3]);
-      } else {
-        const int64_t ld = p_rows;
-        float* o = static_cast<float*>(p_out) + static_cast<int64_t>((kRng ? p_group * p_ranks : 0) + c4 * 4) * ld + grow;
-        if (kRng && stage0 > 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] += o[i * ld];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i * ld] = f[i];
-      }
+      const int64_t ld = p_rows;
+      float* o = static_cast<float*>(p_out) + static_cast<int64_t>(kRng ? p_group * p_ranks : 0) * ld;
+      o[static_cast<int64_t>(c4 * 4 + 0) * ld + grow] = t.x * sc;
+      o[static_cast<int64_t>(c4 * 4 + 1) * ld + grow] = t.y * sc;
+      o[static_cast<int64_t>(c4 * 4 + 2) * ld + grow] = t.z * sc;
+      o[static_cast<int64_t>(c4 * 4 + 3) * ld + grow] = t.w * sc;
     }
   }
   if (ks > 1) cluster_sync_all();                                    // no CTA leaves while others read it

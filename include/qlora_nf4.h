@@ -355,7 +355,7 @@ int qlora_linear_bwd_dropout(const uint16_t* dh, const uint16_t* x, const uint16
  *   from du in full fp32 precision (three bf16 parts), not from bf16(du):
  *   dA and dB are the fp32 sums of exact products to about 1e-6 of the sum of
  *   their absolute values, however many tokens there are (no running sum takes
- *   more than 32 steps of the tensor cores, which cut at each).
+ *   more than 64 steps of the tensor cores, which cut at each).
  *
  * rng        device uint64 [2] {seed, offset}, 8-byte aligned, read when the
  *            kernels run

@@ -360,9 +360,10 @@ def test_gradients_of_long_batches(cuda_lib, M, r):
     """The error of dA and dB does not grow with the tokens.  Positive data,
     where cut bits add up: dh and B are whole numbers up to 15, so that du is
     exact, and q = 1/2, s = 1 are powers of two.  What is left, in units of
-    2^-23 of the sum: an accumulator takes at most 32 steps, each cutting less
-    than one; the rounded additions, half each, are those of at most 8
-    accumulators, 8 x 3 partial tiles and one launch per 8192 tokens or more."""
+    2^-23 of the sum: an accumulator takes at most 64 steps, each cutting less
+    than one of its sum so far, which is half the whole on average; the rounded
+    additions, half each, are those of at most 8 accumulators, 8 x 3 partial
+    tiles and at most one launch per 8192 tokens."""
     q = cuda_lib
     g = torch.Generator(device="cuda").manual_seed(M + r)
     n = 64
