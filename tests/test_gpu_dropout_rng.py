@@ -413,3 +413,10 @@ def test_du_of_many_features_and_tokens(cuda_lib):
     print("du", err, tol)
     assert err <= tol
     assert q.last_device_status() == 0
+
+
+@pytest.mark.parametrize("M,n_in,n_out,r", [(20, 256, 40000, 16), (9, 1088, 8256, 16), (100, 1088, 8256, 12),
+                                            (200, 256, 20032, 8)])
+def test_layer_with_ctas_over_several_row_tiles(cuda_lib, M, n_in, n_out, r):
+    """Few tokens and more row tiles than the SMs' even shares (148 SMs)."""
+    run(cuda_lib, M, n_in, n_out, r, 32.0, 0.1, seed=M)

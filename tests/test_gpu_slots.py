@@ -292,3 +292,54 @@ def test_long_rows_refill_the_operand_ring(cuda_lib, M, n_in, n_out):
     ids_t = torch.from_numpy(ids.astype(np.int32)).cuda()
     for _ in range(20):
         assert torch.equal(h0, q.linear_fwd_slots(x, w, A, B, scale, ids_t))
+
+
+# Shapes whose row tiles are more than the SMs' even shares, on 148 SMs: CTAs
+# begin and end inside tiles, hold the end of one and the start of another
+# (1088 columns: tiles of six units over two to four CTAs) or whole tiles
+# between two cut ones (256 columns: tiles of one or two units).
+@pytest.mark.parametrize("M,n_in,n_out,r,n", [
+    (1, 4096, 4096, 16, 3),
+    (64, 1088, 8256, 16, 13),
+    (100, 1088, 8256, 12, 4),
+    (200, 1088, 8256, 24, 5),
+    (20, 256, 40000, 16, 3),
+    (100, 256, 40000, 8, 5),
+    (200, 256, 40000, 16, 3),
+])
+def test_ctas_over_several_row_tiles(cuda_lib, M, n_in, n_out, r, n):
+    check(cuda_lib, M, n_in, n_out, r, n, mixed(M, n, seed=M) if M > 1 else [1], seed=M)
+
+
+@pytest.mark.parametrize("M", [9, 90, 180])
+def test_base_alone_over_several_row_tiles(cuda_lib, M):
+    check(cuda_lib, M, 256, 40000, 16, 3, np.full(M, -1), seed=M)
+
+
+@pytest.mark.parametrize("M,n_in,n_out", [(12, 256, 40000), (100, 256, 40000), (200, 256, 40000),
+                                          (12, 1088, 8256), (100, 1088, 8256), (200, 1088, 8256)])
+def test_a_broken_adapter_in_whole_and_cut_row_tiles(cuda_lib, M, n_in, n_out):
+    """Infinite and NaN B values in one adapter, in two of any three row tiles:
+    they reach that adapter's tokens in their own features, and nothing else."""
+    q = cuda_lib
+    W, x, A, B, scale = make(M, n_in, n_out, 16, 4, seed=M)
+    ids_n = mixed(M, 4, M)
+    ids_n[:2] = [2, 1]
+    ids = torch.from_numpy(ids_n.astype(np.int32)).cuda()
+    w, x, A, scale = q.quantize_nf4(W.cuda()), x.cuda(), A.cuda(), scale.cuda()
+    h0 = q.linear_fwd_slots(x, w, A, B.cuda(), scale, ids)
+    first = torch.arange(0, n_out, 128)
+    inf_rows = torch.cat([(first + 5)[0::3], (first + 63)[1::3]])
+    nan_rows = (first + 31)[1::3]
+    B[2, inf_rows, 3] = float("inf")
+    B[2, nan_rows, 15] = float("nan")
+    h1 = q.linear_fwd_slots(x, w, A, B.cuda(), scale, ids)
+    mine = torch.from_numpy(ids_n == 2).cuda()
+    touched = torch.zeros(n_out, dtype=torch.bool, device="cuda")
+    touched[inf_rows.cuda()] = touched[nan_rows.cuda()] = True
+    assert torch.equal(h0[~mine], h1[~mine])
+    assert torch.equal(h0[mine][:, ~touched], h1[mine][:, ~touched])
+    assert not bool(h1[mine][:, touched].isfinite().any())
+    assert bool(h1[mine][:, nan_rows.cuda()].isnan().all())
+    assert torch.equal(h1.isnan(), q.linear_fwd_slots(x, w, A, B.cuda(), scale, ids).isnan())
+    assert q.last_device_status() == 0
