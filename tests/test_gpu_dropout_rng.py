@@ -420,3 +420,17 @@ def test_du_of_many_features_and_tokens(cuda_lib):
 def test_layer_with_ctas_over_several_row_tiles(cuda_lib, M, n_in, n_out, r):
     """Few tokens and more row tiles than the SMs' even shares (148 SMs)."""
     run(cuda_lib, M, n_in, n_out, r, 32.0, 0.1, seed=M)
+
+
+def test_keep_bits_of_more_than_2_32_words(cuda_lib):
+    """A mask of 17 GB: the last rows lie past 2^32 words."""
+    M, n, seed, offset, p = 2 ** 21 + 3, 65600, 12, 34, 0.25
+    got = cuda_lib.dropout_keep_bits(rng_tensor(seed, offset), p, M, n)
+    assert got.numel() // 4 > 2 ** 32
+    for m in (0, 2 ** 20 + 1, M - 1):
+        groups = list(range(0, n // 8, 97)) + [n // 8 - 1]
+        row = got[m].cpu().numpy()
+        for g in groups:
+            w = philox.philox4x32((g, m, offset, 0), (seed, 0), 7)
+            bits = sum((((w[i // 2] >> (16 * (i % 2))) & 0xFFFF) >= philox.threshold(p)) << i for i in range(8))
+            assert row[g] == bits, (m, g)

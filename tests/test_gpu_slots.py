@@ -343,3 +343,25 @@ def test_a_broken_adapter_in_whole_and_cut_row_tiles(cuda_lib, M, n_in, n_out):
     assert bool(h1[mine][:, nan_rows.cuda()].isnan().all())
     assert torch.equal(h1.isnan(), q.linear_fwd_slots(x, w, A, B.cuda(), scale, ids).isnan())
     assert q.last_device_status() == 0
+
+
+@pytest.mark.parametrize("M", [20, 200, 300])
+def test_tables_of_more_than_2_31_values(cuda_lib, M):
+    """The last slot of an A table, then of a B table, past 2^31 values: the
+    same bits as with that adapter in a table of 40 (more than 32, so that both
+    calls form us the same way)."""
+    q = cuda_lib
+    r, n = 32, 2400
+    for n_in, n_out in ((28672, 64), (64, 28672)):
+        W, x, A, B, scale = (t.cuda() for t in make(M, n_in, n_out, r, 1, seed=M))
+        w = q.quantize_nf4(W)
+        ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+        want = q.linear_fwd_slots(x, w, A.repeat(40, 1, 1), B.repeat(40, 1, 1), scale.repeat(40), ids)
+        big_a = torch.zeros(n, r, n_in, dtype=torch.bfloat16, device="cuda")
+        big_b = torch.zeros(n, n_out, r, dtype=torch.bfloat16, device="cuda")
+        assert max(big_a.numel(), big_b.numel()) > 2 ** 31
+        big_a[-1], big_b[-1] = A[0], B[0]
+        got = q.linear_fwd_slots(x, w, big_a, big_b, scale.repeat(n), ids + n - 1)
+        assert torch.equal(got, want)
+        del big_a, big_b
+    assert q.last_device_status() == 0
