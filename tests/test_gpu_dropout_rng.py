@@ -434,3 +434,29 @@ def test_keep_bits_of_more_than_2_32_words(cuda_lib):
             w = philox.philox4x32((g, m, offset, 0), (seed, 0), 7)
             bits = sum((((w[i // 2] >> (16 * (i % 2))) & 0xFFFF) >= philox.threshold(p)) << i for i in range(8))
             assert row[g] == bits, (m, g)
+
+
+def test_outputs_of_more_than_2_31_values(cuda_lib):
+    """h and dx past 2^31 values without a mask (p = 0): the last 512 tokens
+    against calls on them alone, bit for bit."""
+    q = cuda_lib
+    M, r = 512 * 157, 8
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for n_in, n_out in ((64, 28672), (28672, 64)):
+        prob = synth.problem(1, n_in, n_out, r, seed=4)
+        w, A, B = q.quantize_nf4(prob["W"].cuda()), prob["A"].cuda(), prob["B"].cuda()
+        rng = rng_tensor(1, 1)
+        x = torch.randn(M, n_in, generator=g, device="cuda").bfloat16()
+        h, us = q.linear_fwd_dropout_rng(x, w, A, B, 16.0, rng, 0.0)
+        t = x[-512:].contiguous()
+        h1, us1 = q.linear_fwd_dropout_rng(t, w, A, B, 16.0, rng, 0.0)
+        us_same = torch.equal(us[-512:], us1)       # (K may be split differently)
+        assert us_same or (us[-512:].float() - us1.float()).norm() <= 2.0 ** -8 * us1.float().norm()
+        assert not us_same or torch.equal(h[-512:], h1)
+        dh = torch.randn(M, n_out, generator=g, device="cuda").bfloat16()
+        dx, _, _ = q.linear_bwd_dropout_rng(dh, x, us, w, torch.zeros_like(A), B, 16.0, rng, 0.0)
+        dx1, _, _ = q.linear_bwd_dropout_rng(dh[-512:].contiguous(), t, us1, w, torch.zeros_like(A), B, 16.0, rng, 0.0)
+        assert torch.equal(dx[-512:], dx1)
+        assert max(h.numel(), dx.numel()) > 2 ** 31
+        del x, h, dh, dx
+    assert q.last_device_status() == 0

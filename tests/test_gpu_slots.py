@@ -365,3 +365,21 @@ def test_tables_of_more_than_2_31_values(cuda_lib, M):
         assert torch.equal(got, want)
         del big_a, big_b
     assert q.last_device_status() == 0
+
+
+def test_outputs_of_more_than_2_31_values(cuda_lib):
+    """The last 512 tokens of a batch whose output passes 2^31 values, against
+    a call on them alone: the same bits."""
+    q = cuda_lib
+    M, n_in, n_out, r, n = 512 * 157, 64, 28672, 8, 5
+    g = torch.Generator(device="cuda").manual_seed(3)
+    W, _, A, B, scale = (t.cuda() for t in make(1, n_in, n_out, r, n, seed=3))
+    x = torch.randn(M, n_in, generator=g, device="cuda").bfloat16()
+    ids = torch.randint(-1, n, (M,), generator=g, device="cuda").int()
+    w = q.quantize_nf4(W)
+    h = q.linear_fwd_slots(x, w, A, B, scale, ids)
+    assert h.numel() > 2 ** 31
+    for k in (-512, 512 * 149):                     # (token 149 * 512 begins just below 2^31)
+        part = slice(k, k + 512 if k > 0 else None)
+        assert torch.equal(h[part], q.linear_fwd_slots(x[part].contiguous(), w, A, B, scale, ids[part].contiguous()))
+    assert q.last_device_status() == 0
