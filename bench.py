@@ -77,8 +77,8 @@ def load_peaks():
         return dict(FALLBACK_PEAKS), "fallback"
 
 
-# sources of the fused dequant GEMM kernels (the dominant kernel of the step)
-GEMM_SOURCES = ("common.cuh", "gemm_pair_sm100.cuh", "gemm_sm100.cuh")
+# sources of the fused dequant GEMM kernels (the dominant kernel of the step), with all that they include
+GEMM_SOURCES = ("common.cuh", "fewtok.cuh", "gemm_pair_sm100.cuh", "gemm_sm100.cuh", "philox.cuh", "slots.cuh")
 
 
 def source_hash(names=GEMM_SOURCES):

@@ -4,6 +4,7 @@ zero-copy end-to-end fields) without touching a GPU."""
 
 import json
 import os
+import re
 import subprocess
 import sys
 
@@ -26,3 +27,19 @@ def test_reference_arm_json_line():
     assert d["cpu_baseline"]["kind"] == "oracle" and d["cpu_baseline"]["value"] == d["value"]
     assert d["e2e"]["h2d_bytes_per_step"] == 0 and d["e2e"]["d2h_bytes_per_step"] == 0
     assert d["config"]["workload"].startswith("llama65b-decoder-layer")
+
+
+def test_traffic_record_covers_every_source_of_the_gemms():
+    """The DRAM record of the dequant GEMMs is dropped when their sources
+    change: the hash covers the two kernels and all that they include."""
+    sys.path.insert(0, ROOT)
+    import bench
+    csrc = os.path.join(ROOT, "bit_nf4_quantized_11_b200", "csrc")
+    todo, seen = ["gemm_pair_sm100.cuh", "gemm_sm100.cuh"], set()
+    while todo:
+        name = todo.pop()
+        if name not in seen:
+            seen.add(name)
+            with open(os.path.join(csrc, name)) as f:
+                todo += re.findall(r'#include "([^"]+)"', f.read())
+    assert seen == set(bench.GEMM_SOURCES)
