@@ -951,6 +951,8 @@ constexpr int64_t kSlotsFewTokens = qnf4::kSgMaxN;
 // rank 16: 12 / 15; 64 tokens of one, 4096, rank 64: 14 / 13; 256 tokens of 2,
 // 4096, rank 64: 30 / 14; 128 tokens of 32, 4096, rank 64: 19 / 17; 256 tokens
 // of 64, 8192, rank 64: 39 / 54; 256 tokens of 256, 4096, rank 16: 18 / 37.
+// The adapters in use are on the device, so the size of the table stands for
+// them: 256 tokens of 2, rank 64, out of a table of more than 32 take the 30.
 bool slots_us_per_token(int64_t M, int64_t n_adapters, int r8) {
   return M <= kSlotsFewTokens && (M * r8 <= 4096 || n_adapters > 32);
 }

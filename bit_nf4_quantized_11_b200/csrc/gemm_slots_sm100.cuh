@@ -34,7 +34,8 @@
 // one copy per lane: a pair of weights takes one prmt (the address), one
 // 8-byte shared load, one packed fp32 multiply and one conversion, and every
 // weight is bf16(level * scale) as everywhere else.  Under that load every
-// shared-memory access (a barrier poll too) takes about 300 clocks, so the
+// shared-memory access (a barrier poll too) takes about 300 clocks (counted
+// likewise), so the
 // chain of a block counts: its lookups go out in four batches of 8, the next
 // one before the last is converted, and the barriers ahead are polled before
 // the last batches and looked at behind them.
@@ -50,7 +51,8 @@
 // A stage is KB = 4 blocks of K (2 above 64 tokens, where two stages of x
 // would not fit otherwise).  The issuing warp runs its loop as a whole, with
 // one elected lane inside the instruction: its operands then stay uniform and
-// an UMMA of 16 tokens issues in 10 clocks; from a one-lane branch it took 118.
+// an UMMA of 16 tokens issues in 10 clocks; from a one-lane branch it took 118
+// (clock counters around the loop, in a build for it).
 // Every wait is bounded, as in gemm_sm100.cuh; no TMA multicast.
 #pragma once
 

@@ -188,7 +188,8 @@ __device__ __noinline__ float slots_odd_term(const uint16_t* B_row, const uint16
 // adapter go in fours, in token order: the CTA of the first of four reads the
 // adapter once for all of them, the other three leave (128 tokens of 64
 // adapters, 28672 wide, rank 16: 31 us each for itself, 24 so; the adapters'
-// and x's bytes out of L2 bound it).  A token's sum is the same in any
+// and x's bytes out of L2 bound it; at three CTAs per SM its registers spill
+// 140 bytes).  A token's sum is the same in any
 // company.  us has rows of r8 = r
 // rounded up to 8; its columns past r, and the rows of tokens without an
 // adapter, are zero.  The CTAs also zero the tickets of the GEMM behind, and
