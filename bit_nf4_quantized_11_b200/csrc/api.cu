@@ -593,10 +593,10 @@ LrShape lr_shape(int64_t tiles, int64_t stages, int N, bool b_mn_major) {
   return sh;
 }
 
-template <bool kCol, bool kBMN, bool kRng = false>
+template <bool kCol, bool kBMN, bool kRng = false, bool kRounds = false>
 int launch_lora_umma(const CUtensorMap (&tm)[4], const qnf4::LrArgs& a, int ks, unsigned grid_x, const char* name,
                      cudaStream_t st) {
-  auto kern = qnf4::lora_umma_kernel<kCol, kBMN, kRng>;
+  auto kern = qnf4::lora_umma_kernel<kCol, kBMN, kRng, kRounds>;
   int smem = qnf4::lr_smem_bytes(a.N, kBMN, a.ring);
   // no other CTA with tensor memory (72 KB or more each) beside those that
   // already share all 512 columns
@@ -1168,7 +1168,9 @@ int lr_rng_accumulators(int N, int n_alloc) { return std::max(1, std::min(8, n_a
 
 // Ring, tensor memory and cluster of the launches whose sums are kept to fp32
 // (du, dA, dB; N-major B): at most `most` stages (4 steps of the tensor cores'
-// sum each) per accumulator, as far as a cluster of 8 goes.
+// sum each) per accumulator, as far as a cluster of 8 goes.  24 for du: the
+// cluster of 8 that 16 asks for takes 78 us where one of 4 takes 70 (8192
+// tokens, 22016 features, rank 64).
 // There are two accumulators at least: N <= 64 where two CTAs share an SM's
 // tensor memory, N <= 256 of all of it otherwise.  Returns the cluster's CTAs.
 int lr_rng_split(qnf4::LrArgs& a, int64_t tiles, int64_t stages, int most) {
@@ -1224,7 +1226,7 @@ int launch_du_parts(const uint16_t* dh, const uint16_t* B, uint16_t* du, int64_t
   a.p[1] = a.p[0];
   a.timeout_ns = g_timeout_ns.load();
   const int64_t stages = cdiv(out, 64);
-  const int ks = lr_rng_split(a, tiles, stages, qnf4::kLrRound);
+  const int ks = lr_rng_split(a, tiles, stages, 24);
   a.stages_per_split = static_cast<int>(cdiv(stages, ks));
   CUtensorMap tm[4];
   if (!make_tmap_bf16(&tm[0], dh, M, out, 128) || !make_tmap_bf16(&tm[1], B, out, r, 64)) return QLORA_ERR_CUDA;
@@ -1256,7 +1258,10 @@ int launch_grads_rng(const uint16_t* dh, const uint16_t* us, const uint16_t* x, 
   if (!make_tmap_bf16(&tm[0], dh, M, out, 64) || !make_tmap_bf16(&tm[1], us, M, r, 64) ||
       !make_tmap_bf16(&tm[2], x, M, in, 64) || !make_tmap_bf16(&tm[3], du, M, cols, 64))
     return QLORA_ERR_CUDA;
-  return launch_lora_umma<true, true, true>(tm, a, ks, static_cast<unsigned>(t_dB + t_dA), "lora_colwise", st);
+  const auto launch = a.stages_per_split > qnf4::kLrRound * lr_rng_accumulators(a.N, a.n_alloc)
+                          ? launch_lora_umma<true, true, true, true>
+                          : launch_lora_umma<true, true, true>;
+  return launch(tm, a, ks, static_cast<unsigned>(t_dB + t_dA), "lora_colwise", st);
 }
 
 // Forward workspace: for few tokens those of the transposed GEMM, then the

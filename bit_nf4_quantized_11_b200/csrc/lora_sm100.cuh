@@ -120,8 +120,9 @@ __host__ __device__ constexpr int lr_smem_bytes(int N, bool b_mn_major, int stag
 }
 
 // kCol: col form (A MN-major, output fp32); otherwise row form (A K-major,
-// output bf16).  kBMN: B operand N-major.
-template <bool kCol, bool kBMN, bool kRng = false>
+// output bf16).  kBMN: B operand N-major.  kRounds (kRng, col form): a CTA may
+// have more than kLrRound stages per accumulator.
+template <bool kCol, bool kBMN, bool kRng = false, bool kRounds = false>
 __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
     const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1, const LrArgs args) {
@@ -177,10 +178,11 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
   const int st_end = min(n_stages_total, st_begin + args.stages_per_split);
   const int n_iter = max(0, st_end - st_begin);
   const uint64_t tmo = args.timeout_ns;
-  const bool in_rounds = kRng && kCol && n_acc > 1 && n_iter > kLrRound * n_acc;
+  // (kRounds) accumulators in use, stages of a round, rounds
+  const bool in_rounds = kRounds && n_acc > 1 && n_iter > kLrRound * n_acc;
   const int n_live = in_rounds ? n_acc - 1 : n_acc;
-  const int round = in_rounds ? kLrRound * n_live : max(1, n_iter);  // stages of a round
-  const int n_rounds = (max(1, n_iter) + round - 1) / round;
+  const int round = in_rounds ? kLrRound * n_live : n_iter;
+  const int n_rounds = in_rounds ? (n_iter + round - 1) / round : 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -189,8 +191,10 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
       mbar_init(masked + s, (blockDim.x - 64) / 32);                 // one arrive per masking warp
     }
     mbar_init(acc_full, 1);
-    mbar_init(round_full, 1);
-    mbar_init(round_empty, 8);                                       // the masking warps
+    if (kRounds) {
+      mbar_init(round_full, 1);
+      mbar_init(round_empty, 8);                                     // the masking warps
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -275,15 +279,16 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     if (lane == 0) {
       // ------------------------------------------------------------ MMA issuer
       const uint32_t idesc = umma_idesc_bf16_ab(kLrTileRows, p_N, kCol, kBMN);
-      int turn = 0, rounds_done = 0;                                 // (kRng) the stage within its round
-      for (int it = 0; it < n_iter; ++it, ++turn) {
+      int lo = 0, rounds_done = 0;                                   // (kRounds) the round's first stage
+      for (int it = 0; it < n_iter; ++it) {
         const int s = it % S;
-        if (kRng && kCol && turn == round) {
+        if (kRounds && it - lo == round) {
           umma_commit(round_full);
           wait(round_empty, rounds_done & 1u);
           ++rounds_done;
-          turn = 0;
+          lo = it;
         }
+        const int turn = kRounds ? it - lo : it;
         wait(full + s, (it / S) & 1u);
         if (do_mask) wait(masked + s, (it / S) & 1u);
         if (*abort_flag) break;
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
       const uint32_t row_off = (kCol ? (i >> 6) * 8192 : 0) + r * 128;
       for (int it = 0; it < n_iter; ++it) {
         const int s = it % S;
-        if (kCol && it > 0 && it % round == 0 && !end_round(it / round - 1)) break;
+        if (kRounds && it > 0 && it % round == 0 && !end_round(it / round - 1)) break;
         const int k0 = (st_begin + it) * 64;
         const int tok = kCol ? k0 + (i & 63) : row0 + i;
         const int f0 = kCol ? row0 + 64 * (i >> 6) : k0;
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(masked + s);
     }
-  } else if (kRng && kCol) {
+  } else if (kRounds) {
     for (int k = 0; k + 1 < n_rounds && end_round(k); ++k) {}
   }
 
@@ -448,16 +453,16 @@ __global__ void __launch_bounds__(kLrMaskThreads) lora_umma_kernel(
     tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + c0, v);
     tmem_ld_wait();
     if (kRng) {
-      // the last round's accumulators, then the total of the rounds before
-      const int n_sets = min(n_live, n_iter - (n_rounds - 1) * round);
-      for (int e = 1; e < n_sets + (n_rounds > 1 ? 1 : 0); ++e) {
-        const int g = e < n_sets ? e : n_live;
+      auto add = [&](int g) {
         uint32_t w[32];
         tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + g * acc_stride + c0, w);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
-      }
+      };
+      const int n_last = kRounds ? n_iter - (n_rounds - 1) * round : n_iter;       // stages of the last round
+      for (int g = 1; g < n_live && g < n_last; ++g) add(g);
+      if (kRounds && n_rounds > 1) add(n_live);                      // the total of the rounds before
     }
     if (n_iter == 0) {
 #pragma unroll

@@ -355,8 +355,8 @@ int qlora_linear_bwd_dropout(const uint16_t* dh, const uint16_t* x, const uint16
  *   from du in full fp32 precision (three bf16 parts), not from bf16(du):
  *   dA and dB are the fp32 sums of exact products to about 1e-6 of the sum of
  *   their absolute values, however many tokens there are: no running sum takes
- *   more than 64 steps of the tensor cores, which cut at each.  The same holds
- *   for du's sum over out up to out = 32768 for r <= 128, 16384 for any r.
+ *   more than 64 steps of the tensor cores, which cut at each.  du's sum over
+ *   out takes 96 at most up to out = 49152 for r <= 128, 24576 for any r.
  *   dx = bf16(dh W0 + (bf16(du) A) k / (1 - q)), rounded once for r <= 80; for
  *   more ranks dh W0 is rounded to bf16 before the other term is added.  A
  *   dropped value of dx is dh W0 alone, whatever the adapter holds.
