@@ -363,7 +363,7 @@ def test_gradients_of_long_batches(cuda_lib, M, r):
     2^-23 of the sum: an accumulator takes at most 64 steps, each cutting less
     than one of its sum so far, which is half the whole on average; the rounded
     additions, half each, are those of at most 8 accumulators, 8 x 3 partial
-    tiles and at most one launch per 8192 tokens."""
+    tiles and at most one round per 8192 tokens."""
     q = cuda_lib
     g = torch.Generator(device="cuda").manual_seed(M + r)
     n = 64
