@@ -355,7 +355,8 @@ def test_a_dropped_column_of_dx_is_the_base_product(cuda_lib, M, r):
     assert torch.equal(dx[~keep], base[~keep]) and bool(dx[keep].isnan().all())
 
 
-@pytest.mark.parametrize("M,r", [(8193, 64), (20000, 136), (40000, 16), (100001, 64), (262144, 64)])
+@pytest.mark.parametrize("M,r", [(8193, 64), (20000, 136), (33000, 80), (33000, 256), (40000, 16), (70000, 12),
+                                 (100001, 64), (262144, 64)])
 def test_gradients_of_long_batches(cuda_lib, M, r):
     """The error of dA and dB does not grow with the tokens.  Positive data,
     where cut bits add up: dh and B are whole numbers up to 15, so that du is
